@@ -24,10 +24,11 @@
  *    means nothing was launched. T = 0 is valid and enqueues nothing.
  *  - Shape limits: 1 <= E <= 1024, 1 <= top_k <= min(E, 32), T*top_k < 2^31;
  *    H and I multiples of 8 (multiples of 128 for MOE_W_INT4_G128,
- *    MOE_W_MXFP8 and MOE_W_MXFP4).
+ *    MOE_W_MXFP8 and MOE_W_MXFP4; multiples of 16 up to 32768 for
+ *    MOE_W_INT8).
  *  - Weight scales are passed as untyped pointers: bf16 [rows, K/128] for
  *    MOE_W_INT4_G128, E8M0 bytes [rows, K/32] for MOE_W_MXFP8 and
- *    MOE_W_MXFP4, NULL for bf16. Device pointers must be 16-byte aligned
+ *    MOE_W_MXFP4, fp32 [rows] for MOE_W_INT8, NULL for bf16. Device pointers must be 16-byte aligned
  *    (32-byte for MOE_W_MXFP4 weights; 4-byte for logits/topk_w and the
  *    int32 arrays).
  *  - Pair ids: p = t*K + j for token t and slot j, with K = top_k +
@@ -73,8 +74,10 @@ typedef enum {
     MOE_W_INT4_G128 = 1,   /* W4A16: int4 weights, one bf16 scale per 128 K */
     MOE_W_MXFP8 = 2,       /* MXFP8 (OCP MX v1.0): E4M3 weights, one E8M0 scale per 32 K;
                               the activations are MX-quantised by the layer */
-    MOE_W_MXFP4 = 3        /* MXFP4 weights (OCP MX v1.0 E2M1, two per byte, even K in the
+    MOE_W_MXFP4 = 3,       /* MXFP4 weights (OCP MX v1.0 E2M1, two per byte, even K in the
                               low nibble, one E8M0 scale per 32 K) with MXFP8 activations */
+    MOE_W_INT8 = 4         /* W8A8: int8 weights, one fp32 scale per weight row (output channel);
+                              the activations are int8 with one fp32 scale per token row */
 } moe_weight_fmt_t;
 
 /* Layer shape. T tokens, hidden size H, expert intermediate size I, E routed
@@ -120,6 +123,71 @@ MOE_API size_t moe_permute_workspace_size(const moe_shape_t *shape);
  *            each shared slot. */
 MOE_API moe_status_t moe_route(const float *logits, const moe_shape_t *shape,
                        int32_t *topk_ids, float *topk_w, moe_stream_t stream);
+
+/* Routing by scores: softmax or sigmoid of the router logits, a selection
+ * bias per expert (used to balance the expert load), expert groups, weights
+ * renormalised or not. For the logits l of one token (NaN counts as -inf, -0
+ * as +0) and the bias b:
+ *   MOE_SCORE_SOFTMAX  s_e = exp(l_e - m) / sum_i exp(l_i - m), m = max l;
+ *                      logits that equal m = +inf share the sum, and s = 0
+ *                      when every logit is -inf
+ *   MOE_SCORE_SIGMOID  s_e = 1 / (1 + exp(-l_e))
+ *   selection          c_e = s_e + b_e, formed and compared in 64 bits (NaN
+ *                      counts as -inf). Without a bias (bias = NULL) the
+ *                      order is that of the logits, compared exactly.
+ *   groups             n_group groups of E / n_group consecutive experts. A
+ *                      group's value is the sum of its group_top (1 or 2)
+ *                      largest c (s without a bias); the topk_group groups
+ *                      of the largest values stay, equal ones by the lower
+ *                      index.
+ *   ids                the top_k largest c in those groups in descending
+ *                      order, equal ones by the lower expert id
+ *   weights            w_j = scale * s_j / sum of the selected s when
+ *                      renormalize is 1, scale * s_j when it is 0: the bias
+ *                      does not enter. A selected expert whose bias is -inf
+ *                      (or NaN) has weight 0, and when the selected scores
+ *                      are all 0 so are the weights.
+ * Shared slots follow with weight 1, not scaled.
+ *   1 <= topk_group <= n_group <= 32, E a multiple of n_group, group_top <=
+ *   E / n_group (with more than one group), top_k <= topk_group * E / n_group,
+ *   scale finite. */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
+typedef enum { MOE_LOGITS_FP32 = 0, MOE_LOGITS_BF16 = 1 } moe_logits_t;
+typedef struct {
+    int32_t logits;        /* a moe_logits_t: the type of the logits array */
+    int32_t score;         /* a moe_score_t */
+    int32_t n_group;       /* expert groups (1: no groups) */
+    int32_t topk_group;    /* groups kept per token */
+    int32_t group_top;     /* 1 or 2: scores summed for a group's value */
+    int32_t renormalize;   /* 0 or 1 */
+    float scale;           /* factor of the routed weights */
+} moe_router_t;
+
+/* logits [T,E] fp32 or bf16 (router->logits), bias [E] fp32 or NULL; topk_ids
+ * and topk_w as moe_route's. One warp per token; weights in fp32 (expf, sum
+ * in slot order). */
+MOE_API moe_status_t moe_route_scored(const void *logits, const float *bias, const moe_router_t *router,
+                                      const moe_shape_t *shape, int32_t *topk_ids, float *topk_w,
+                                      moe_stream_t stream);
+
+/* RMS norm with the residual's addition, and the rows the layer takes:
+ *   h = x + residual in fp32, residual_out = bf16(h)
+ *   y = h / sqrt(sum_i h_i^2 / H + eps) * weight in fp32, from the unrounded h
+ * x [rows,H] bf16, weight [H] bf16, eps > 0 and finite. residual and
+ * residual_out [rows,H] bf16 are given together or are both NULL (h = x).
+ * fmt, a moe_weight_fmt_t, says what the layer behind it reads:
+ *   MOE_W_BF16, MOE_W_INT4_G128  y [rows,H] bf16; q and scales NULL; H % 8 == 0
+ *   MOE_W_MXFP8, MOE_W_MXFP4     q [rows,H] E4M3 and scales [rows,H/32] E8M0 of
+ *                                y by moe_mx_quantize's rule; H % 32 == 0
+ *   MOE_W_INT8                   q [rows,H] int8 and scales [rows] fp32 of y by
+ *                                moe_i8_quantize's rule; H % 16 == 0
+ * y [rows,H] bf16 may also be given with the 8-bit forms (the router's input),
+ * or be NULL. The 8-bit forms are taken from the fp32 y, not from its bf16
+ * rounding. residual_out may be x or residual itself, and so may y; other
+ * overlaps are not allowed. H <= 32768. */
+MOE_API moe_status_t moe_rmsnorm(const moe_bf16_t *x, const moe_bf16_t *residual, const moe_bf16_t *weight, float eps,
+                                 int32_t rows, int32_t H, int32_t fmt, moe_bf16_t *residual_out, moe_bf16_t *y,
+                                 void *q, void *scales, moe_stream_t stream);
 
 /* Permute (bucketing). InfiniLM PR #500 report §2.2 step 1 (per-expert counts
  * and a permutation) and step 2 (gather by that permutation), done on the
@@ -218,6 +286,15 @@ MOE_API moe_status_t moe_forward(const moe_bf16_t *hidden, const float *logits,
                          const moe_shape_t *shape, moe_bf16_t *out,
                          void *ws, size_t ws_bytes, moe_stream_t stream);
 
+/* moe_forward with moe_route_scored's routing in the place of moe_route's:
+ * logits fp32 or bf16 (router->logits), bias [E] fp32 or NULL. The steps run as
+ * their own kernels for every shape and weight format; the result equals the
+ * step entry points called in that order. Workspace as moe_forward's. */
+MOE_API moe_status_t moe_forward_scored(const moe_bf16_t *hidden, const void *logits, const float *bias,
+                                        const moe_router_t *router, const void *w_gu, const void *w_gu_scales,
+                                        const void *w_d, const void *w_d_scales, const moe_shape_t *shape,
+                                        moe_bf16_t *out, void *ws, size_t ws_bytes, moe_stream_t stream);
+
 /* The whole layer for a decode batch in ONE persistent kernel: routing,
  * bucketing, gate/up + SwiGLU, down and finalize, with no kernel boundary
  * between them (the GC-MoE abstract fuses the layer's steps into one graph;
@@ -289,6 +366,36 @@ MOE_API moe_status_t moe_grouped_gemm_swiglu_mx(const uint8_t *a_q, const uint8_
 MOE_API moe_status_t moe_grouped_gemm_down_mx(const uint8_t *act_q, const uint8_t *act_scales,
                                               const int32_t *offsets, const void *w_d, const void *w_d_scales,
                                               const moe_shape_t *shape, moe_bf16_t *y, moe_stream_t stream);
+
+/* Int8 rows (MOE_W_INT8: W8A8). The integer MMA takes both operands as int8,
+ * so the layer quantises its activations row by row: hidden before gate/up,
+ * and act (after its bf16 rounding) before down. moe_forward does all of it;
+ * these are the steps on their own.
+ *
+ * Quantisation of x [rows, K] bf16 (K % 16 == 0, K <= 32768) into q [rows, K]
+ * int8 and scales [rows] fp32: scale = max|x| / 127 over the row, q = 127 x /
+ * max|x| rounded to nearest even, in [-127, 127]; a row of zeros has scale 0,
+ * a row with an infinity or a NaN has q = 0 and scale NaN (every product it
+ * enters is NaN). Bit-exact. */
+MOE_API moe_status_t moe_i8_quantize(const moe_bf16_t *x, int32_t rows, int32_t K, int8_t *q, float *scales,
+                                     moe_stream_t stream);
+
+/* Gate/up + SwiGLU with int8 weights (shape->fmt = MOE_W_INT8):
+ *   a_q, a_scales  perm == NULL: permuted rows [T*top_k, H] / [T*top_k];
+ *                  perm != NULL: hidden's quantisation [T, H] / [T], rows read
+ *                  through perm (TMA gather4)
+ *   w_gu [E,2I,H] int8 (rows [0,I) gate, [I,2I) up), w_gu_scales [E,2I] fp32
+ *   act [T*top_k, I] bf16 out: act = bf16(silu(g) * u), g and u the int32 sums
+ *   times the weight row's scale and the token row's scale in fp32. */
+MOE_API moe_status_t moe_grouped_gemm_swiglu_i8(const int8_t *a_q, const float *a_scales, const int32_t *perm,
+                                                const int32_t *offsets, const void *w_gu, const void *w_gu_scales,
+                                                const moe_shape_t *shape, moe_bf16_t *act, moe_stream_t stream);
+
+/* Down with int8 weights: act_q [T*top_k, I] int8 + act_scales [T*top_k] fp32,
+ * w_d [E,H,I] int8 + w_d_scales [E,H] fp32 -> y [T*top_k, H] bf16. */
+MOE_API moe_status_t moe_grouped_gemm_down_i8(const int8_t *act_q, const float *act_scales, const int32_t *offsets,
+                                              const void *w_d, const void *w_d_scales, const moe_shape_t *shape,
+                                              moe_bf16_t *y, moe_stream_t stream);
 
 /* W4A16 weight decoding on its own (the step the int4 GEMMs run on chip
  * before their MMAs). FlashInfer PR #7196 analysis §2-§3.

@@ -28,6 +28,8 @@ __all__ = [
     "moe_forward_kernel_count", "moe_forward_gathers_in_gemm", "forward", "debug_bounds_library",
     "moe_mx_quantize", "moe_grouped_gemm_swiglu_mx", "moe_grouped_gemm_down_mx", "FMT_MXFP8", "FMT_MXFP4",
     "moe_forward_fused", "moe_forward_is_fused",
+    "FMT_INT8", "Router", "moe_route_scored", "moe_rmsnorm", "moe_i8_quantize", "moe_grouped_gemm_swiglu_i8",
+    "moe_grouped_gemm_down_i8", "moe_forward_scored",
     "EP_MAX_RANKS", "EpPeers", "moe_ep_count", "moe_ep_dispatch", "moe_ep_local_offsets", "moe_ep_combine",
     "ep_forward",
 ]
@@ -39,6 +41,7 @@ FMT_BF16 = 0
 FMT_INT4_G128 = 1
 FMT_MXFP8 = 2
 FMT_MXFP4 = 3
+FMT_INT8 = 4
 
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED",
           3: "MOE_ERR_WORKSPACE_TOO_SMALL", 4: "MOE_ERR_CUDA", 5: "MOE_ERR_DEVICE_FLAG"}
@@ -72,7 +75,8 @@ class Shape(ctypes.Structure):
     @classmethod
     def of(cls, T, H, I, E, top_k, fmt=FMT_BF16, n_shared=0) -> "Shape":
         if isinstance(fmt, str):
-            fmt = {"bf16": FMT_BF16, "int4_g128": FMT_INT4_G128, "mxfp8": FMT_MXFP8, "mxfp4": FMT_MXFP4}[fmt]
+            fmt = {"bf16": FMT_BF16, "int4_g128": FMT_INT4_G128, "mxfp8": FMT_MXFP8, "mxfp4": FMT_MXFP4,
+                   "int8": FMT_INT8}[fmt]
         return cls(int(T), int(H), int(I), int(E), int(top_k), int(fmt), int(n_shared))
 
     @property
@@ -82,6 +86,20 @@ class Shape(ctypes.Structure):
     @property
     def experts(self) -> int:
         return self.E + self.n_shared
+
+
+class Router(ctypes.Structure):
+    """moe_router_t: how moe_route_scored turns router logits into experts and
+    weights (softmax or sigmoid scores, expert groups, renormalisation, scale)."""
+    _fields_ = [("logits", ctypes.c_int32), ("score", ctypes.c_int32), ("n_group", ctypes.c_int32),
+                ("topk_group", ctypes.c_int32), ("group_top", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+    @classmethod
+    def of(cls, score="softmax", n_group=1, topk_group=1, group_top=1, renormalize=True, scale=1.0,
+           logits="fp32") -> "Router":
+        return cls({"fp32": 0, "bf16": 1}[logits], {"softmax": 0, "sigmoid": 1}[score], int(n_group), int(topk_group),
+                   int(group_top), int(bool(renormalize)), float(scale))
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -132,6 +150,7 @@ def _load(debug_bounds: bool) -> ctypes.CDLL:
     L = ctypes.CDLL(path)
     vp, sz, i32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32
     sp = ctypes.POINTER(Shape)
+    rp = ctypes.POINTER(Router)
     sigs = {
         "moe_workspace_size": ([sp], sz),
         "moe_permute_workspace_size": ([sp], sz),
@@ -158,6 +177,12 @@ def _load(debug_bounds: bool) -> ctypes.CDLL:
         "moe_ep_dispatch": ([vp, vp, vp, sp, ctypes.POINTER(EpPeers), vp], ctypes.c_int),
         "moe_ep_local_offsets": ([sp, ctypes.POINTER(EpPeers), vp, vp], ctypes.c_int),
         "moe_ep_combine": ([vp, vp, sp, ctypes.POINTER(EpPeers), vp], ctypes.c_int),
+        "moe_route_scored": ([vp, vp, rp, sp, vp, vp, vp], ctypes.c_int),
+        "moe_rmsnorm": ([vp, vp, vp, ctypes.c_float, i32, i32, i32, vp, vp, vp, vp, vp], ctypes.c_int),
+        "moe_i8_quantize": ([vp, i32, i32, vp, vp, vp], ctypes.c_int),
+        "moe_grouped_gemm_swiglu_i8": ([vp, vp, vp, vp, vp, vp, sp, vp, vp], ctypes.c_int),
+        "moe_grouped_gemm_down_i8": ([vp, vp, vp, vp, vp, sp, vp, vp], ctypes.c_int),
+        "moe_forward_scored": ([vp, vp, vp, rp, vp, vp, vp, vp, sp, vp, vp, sz, vp], ctypes.c_int),
         "moe_status_string": ([ctypes.c_int], ctypes.c_char_p),
     }
     for name, (args, res) in sigs.items():
@@ -169,7 +194,7 @@ def _load(debug_bounds: bool) -> ctypes.CDLL:
 
 # ---- marshalling helpers ---------------------------------------------------
 
-BF16, F32, I32, U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+BF16, F32, I32, U8, I8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.int8
 
 
 def _p(t, *dtypes) -> Optional[int]:
@@ -183,6 +208,23 @@ def _p(t, *dtypes) -> Optional[int]:
         raise TypeError(f"libmoe_b200: expected a tensor of {' or '.join(map(str, dtypes))}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError("tensors passed to libmoe_b200 must be contiguous")
+    return t.data_ptr()
+
+
+def _pd(t, n: int, *dtypes) -> Optional[int]:
+    """_p of a tensor of at least n elements on the current CUDA device (None
+    for None): a host tensor, a tensor of another device or a short one is
+    refused before the library is called. An address (int) passes as it is."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.dtype not in dtypes:
+        raise TypeError(f"libmoe_b200: expected a tensor of {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to libmoe_b200 must be contiguous")
+    if t.numel() < n:
+        raise ValueError(f"libmoe_b200: expected at least {n} elements, got a tensor of shape {tuple(t.shape)}")
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"libmoe_b200: expected a tensor on the current CUDA device, got one on {t.device}")
     return t.data_ptr()
 
 
@@ -225,6 +267,27 @@ def moe_route(logits, shape, topk_ids, topk_w, stream=None) -> None:
            "moe_route")
 
 
+def moe_route_scored(logits, bias, router: Router, shape, topk_ids, topk_w, stream=None) -> None:
+    sh = _shape(shape)
+    T, E, slots = sh.T, sh.E, sh.T * sh.slots
+    _check(lib().moe_route_scored(_pd(logits, T * E, BF16 if router.logits == 1 else F32), _pd(bias, E, F32),
+                                  ctypes.byref(router), ctypes.byref(sh), _pd(topk_ids, slots, I32),
+                                  _pd(topk_w, slots, F32), _s(stream)),
+           "moe_route_scored")
+
+
+def moe_rmsnorm(x, residual, weight, eps: float, rows: int, H: int, fmt, residual_out, y, q=None, scales=None,
+                stream=None) -> None:
+    n = rows * H
+    if fmt == FMT_INT8:
+        q_p, s_p = _pd(q, n, I8), _pd(scales, rows, F32)
+    else:
+        q_p, s_p = _pd(q, n, U8), _pd(scales, n // 32, U8)
+    _check(lib().moe_rmsnorm(_pd(x, n, BF16), _pd(residual, n, BF16), _pd(weight, H, BF16), float(eps), rows, H, fmt,
+                             _pd(residual_out, n, BF16), _pd(y, n, BF16), q_p, s_p, _s(stream)),
+           "moe_rmsnorm")
+
+
 def moe_permute(topk_ids, shape, counts, offsets, perm, inv_perm, hidden=None, hidden_perm=None,
                 ws=None, stream=None) -> None:
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
@@ -265,8 +328,8 @@ def moe_finalize(y, topk_w, inv_perm, shape, out, stream=None) -> None:
 
 def moe_forward(hidden, logits, w_gu, w_gu_scales, w_d, w_d_scales, shape, out, ws, stream=None) -> None:
     nbytes = ws.numel() * ws.element_size()
-    _check(lib().moe_forward(_p(hidden, BF16), _p(logits, F32), _p(w_gu, BF16, U8), _p(w_gu_scales, BF16, U8),
-                             _p(w_d, BF16, U8), _p(w_d_scales, BF16, U8), ctypes.byref(_shape(shape)), _p(out, BF16),
+    _check(lib().moe_forward(_p(hidden, BF16), _p(logits, F32), _p(w_gu, BF16, U8, I8), _p(w_gu_scales, BF16, U8, F32),
+                             _p(w_d, BF16, U8, I8), _p(w_d_scales, BF16, U8, F32), ctypes.byref(_shape(shape)), _p(out, BF16),
                              _p(ws), nbytes, _s(stream)),
            "moe_forward")
 
@@ -274,8 +337,9 @@ def moe_forward(hidden, logits, w_gu, w_gu_scales, w_d, w_d_scales, shape, out, 
 def moe_forward_host(hidden_host, logits_host, w_gu, w_gu_scales, w_d, w_d_scales, shape, out_host, ws,
                      stream=None) -> None:
     nbytes = ws.numel() * ws.element_size()
-    _check(lib().moe_forward_host(_p(hidden_host, BF16), _p(logits_host, F32), _p(w_gu, BF16, U8),
-                                  _p(w_gu_scales, BF16, U8), _p(w_d, BF16, U8), _p(w_d_scales, BF16, U8),
+    _check(lib().moe_forward_host(_p(hidden_host, BF16), _p(logits_host, F32), _p(w_gu, BF16, U8, I8),
+                                  _p(w_gu_scales, BF16, U8, F32), _p(w_d, BF16, U8, I8),
+                                  _p(w_d_scales, BF16, U8, F32),
                                   ctypes.byref(_shape(shape)), _p(out_host, BF16), _p(ws), nbytes, _s(stream)),
            "moe_forward_host")
 
@@ -304,6 +368,55 @@ def moe_grouped_gemm_down_mx(act_q, act_scales, offsets, w_d, w_d_scales, shape,
     _check(lib().moe_grouped_gemm_down_mx(_p(act_q, U8), _p(act_scales, U8), _p(offsets, I32), _p(w_d, U8),
                                           _p(w_d_scales, U8), ctypes.byref(_shape(shape)), _p(y, BF16), _s(stream)),
            "moe_grouped_gemm_down_mx")
+
+
+def moe_i8_quantize(x, rows: int, K: int, q, scales, stream=None) -> None:
+    _check(lib().moe_i8_quantize(_pd(x, rows * K, BF16), rows, K, _pd(q, rows * K, I8), _pd(scales, rows, F32),
+                                 _s(stream)),
+           "moe_i8_quantize")
+
+
+def moe_grouped_gemm_swiglu_i8(a_q, a_scales, perm, offsets, w_gu, w_gu_scales, shape, act, stream=None) -> None:
+    sh = _shape(shape)
+    P, E = sh.T * sh.slots, sh.experts
+    rows = P if perm is None else sh.T
+    _check(lib().moe_grouped_gemm_swiglu_i8(_pd(a_q, rows * sh.H, I8), _pd(a_scales, rows, F32), _pd(perm, P, I32),
+                                            _pd(offsets, E + 1, I32), _pd(w_gu, E * 2 * sh.I * sh.H, I8),
+                                            _pd(w_gu_scales, E * 2 * sh.I, F32), ctypes.byref(sh),
+                                            _pd(act, P * sh.I, BF16), _s(stream)),
+           "moe_grouped_gemm_swiglu_i8")
+
+
+def moe_grouped_gemm_down_i8(act_q, act_scales, offsets, w_d, w_d_scales, shape, y, stream=None) -> None:
+    sh = _shape(shape)
+    P, E = sh.T * sh.slots, sh.experts
+    _check(lib().moe_grouped_gemm_down_i8(_pd(act_q, P * sh.I, I8), _pd(act_scales, P, F32), _pd(offsets, E + 1, I32),
+                                          _pd(w_d, E * sh.H * sh.I, I8), _pd(w_d_scales, E * sh.H, F32),
+                                          ctypes.byref(sh), _pd(y, P * sh.H, BF16), _s(stream)),
+           "moe_grouped_gemm_down_i8")
+
+
+def moe_forward_scored(hidden, logits, bias, router: Router, w_gu, w_gu_scales, w_d, w_d_scales, shape, out, ws,
+                       stream=None) -> None:
+    sh = _shape(shape)
+    T, H, I, E = sh.T, sh.H, sh.I, sh.experts
+    # bytes and scales per weight row of K elements
+    row = {FMT_BF16: (lambda K: K, lambda K: 0, (BF16,), (BF16,)),
+           FMT_INT4_G128: (lambda K: K // 2, lambda K: K // 128, (U8,), (BF16,)),
+           FMT_MXFP8: (lambda K: K, lambda K: K // 32, (U8,), (U8,)),
+           FMT_MXFP4: (lambda K: K // 2, lambda K: K // 32, (U8,), (U8,)),
+           FMT_INT8: (lambda K: K, lambda K: 1, (I8,), (F32,))}
+    if sh.fmt not in row:
+        raise MoeError(1, "moe_forward_scored")
+    codes, scales, w_dt, s_dt = row[sh.fmt]
+    nbytes = ws.numel() * ws.element_size()
+    _check(lib().moe_forward_scored(_pd(hidden, T * H, BF16),
+                                    _pd(logits, T * sh.E, BF16 if router.logits == 1 else F32), _pd(bias, sh.E, F32),
+                                    ctypes.byref(router), _pd(w_gu, E * 2 * I * codes(H), *w_dt),
+                                    _pd(w_gu_scales, E * 2 * I * scales(H), *s_dt), _pd(w_d, E * H * codes(I), *w_dt),
+                                    _pd(w_d_scales, E * H * scales(I), *s_dt), ctypes.byref(sh),
+                                    _pd(out, T * H, BF16), _pd(ws, 0, ws.dtype), nbytes, _s(stream)),
+           "moe_forward_scored")
 
 
 def moe_dequant_int4(q, scales, rows: int, K: int, out, stream=None) -> None:
@@ -347,16 +460,23 @@ def moe_status_string(status: int) -> str:
 
 def forward(hidden: torch.Tensor, logits: torch.Tensor, w_gu: torch.Tensor, w_d: torch.Tensor, top_k: int,
             w_gu_scales: Optional[torch.Tensor] = None, w_d_scales: Optional[torch.Tensor] = None,
-            out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+            out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None,
+            router: Optional[Router] = None, bias: Optional[torch.Tensor] = None) -> torch.Tensor:
     """moe_forward on device tensors; allocates out and the workspace with
     torch when they are not given. hidden [T,H] bf16, logits [T,E] fp32,
     w_gu [E+S,2I,H] bf16 (or uint8: int4 [E+S,2I,H/2] with bf16 scales, MXFP8
-    [E+S,2I,H] or MXFP4 [E+S,2I,H/2] with uint8 scales), w_d likewise:
-    weight arrays with more experts than logits columns hold S shared experts
-    after the E routed ones."""
+    [E+S,2I,H] or MXFP4 [E+S,2I,H/2] with uint8 scales; or int8 [E+S,2I,H] with
+    fp32 scales [E+S,2I]), w_d likewise: weight arrays with more experts than
+    logits columns hold S shared experts after the E routed ones. With a
+    router, moe_forward_scored (logits fp32 or bf16 as the router says, bias
+    [E] fp32 or None)."""
     T, H = hidden.shape
     E = logits.shape[1]
-    if w_gu.dtype != torch.uint8:
+    if bias is not None and router is None:
+        raise ValueError("a selection bias needs a router")
+    if w_gu.dtype == torch.int8:
+        fmt = FMT_INT8
+    elif w_gu.dtype != torch.uint8:
         fmt = FMT_BF16
     elif w_gu_scales is None or w_gu_scales.dtype != torch.uint8:
         fmt = FMT_INT4_G128
@@ -368,7 +488,10 @@ def forward(hidden: torch.Tensor, logits: torch.Tensor, w_gu: torch.Tensor, w_d:
         out = torch.empty(T, H, dtype=torch.bfloat16, device=hidden.device)
     if ws is None:
         ws = torch.empty(max(moe_workspace_size(shape), 1), dtype=torch.uint8, device=hidden.device)
-    moe_forward(hidden, logits, w_gu, w_gu_scales, w_d, w_d_scales, shape, out, ws, stream)
+    if router is not None:
+        moe_forward_scored(hidden, logits, bias, router, w_gu, w_gu_scales, w_d, w_d_scales, shape, out, ws, stream)
+    else:
+        moe_forward(hidden, logits, w_gu, w_gu_scales, w_d, w_d_scales, shape, out, ws, stream)
     return out
 
 

@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <map>
 #include <memory>
 #include <mutex>
@@ -45,17 +46,24 @@ inline int slots(const moe_shape_t *s) { return s->top_k + s->n_shared; }
 inline int experts(const moe_shape_t *s) { return s->E + s->n_shared; }
 // Block-scaled formats: MX weights, MXFP8 activations.
 inline bool is_mx(int fmt) { return fmt == MOE_W_MXFP8 || fmt == MOE_W_MXFP4; }
+inline bool is_i8(int fmt) { return fmt == MOE_W_INT8; }
+// Longest row of the int8 and norm kernels (a row lives in registers; also keeps int32 sums exact).
+constexpr int kMaxRow = 32768;
 
 moe_status_t check_shape(const moe_shape_t *s) {
     if (!s) return MOE_ERR_INVALID_ARG;
     if (s->T < 0 || s->H <= 0 || s->I <= 0 || s->E < 1 || s->top_k < 1 || s->top_k > s->E || s->n_shared < 0)
         return MOE_ERR_INVALID_ARG;
-    if (s->fmt != MOE_W_BF16 && s->fmt != MOE_W_INT4_G128 && s->fmt != MOE_W_MXFP8 && s->fmt != MOE_W_MXFP4)
+    if (s->fmt != MOE_W_BF16 && s->fmt != MOE_W_INT4_G128 && !is_mx(s->fmt) && !is_i8(s->fmt))
         return MOE_ERR_INVALID_ARG;
     if (static_cast<long long>(s->E) + s->n_shared > 1024 || static_cast<long long>(s->top_k) + s->n_shared > 32)
         return MOE_ERR_UNSUPPORTED;
     if (s->H % 8 || s->I % 8) return MOE_ERR_UNSUPPORTED;
-    if (s->fmt != MOE_W_BF16 && (s->H % 128 || s->I % 128)) return MOE_ERR_UNSUPPORTED;
+    if (is_i8(s->fmt)) {
+        if (s->H % 16 || s->I % 16 || s->H > kMaxRow || s->I > kMaxRow) return MOE_ERR_UNSUPPORTED;
+    } else if (s->fmt != MOE_W_BF16 && (s->H % 128 || s->I % 128)) {
+        return MOE_ERR_UNSUPPORTED;
+    }
     if (static_cast<long long>(s->T) * slots(s) >= (1LL << 31)) return MOE_ERR_UNSUPPORTED;
     if (static_cast<long long>(experts(s)) * 2 * s->I >= (1LL << 31) ||
         static_cast<long long>(experts(s)) * s->H >= (1LL << 31))
@@ -67,10 +75,16 @@ moe_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE
 
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
+// Whether the gate/up GEMM of moe_forward reads the token rows through perm.
+bool gathers_in_kernel(const moe_shape_t *s) {
+    const int P = s->T * slots(s), E = experts(s);
+    return is_i8(s->fmt) ? moe::gemm_i8_gathers_in_kernel(P, E) : moe::gemm_gathers_in_kernel(P, E, s->fmt);
+}
+
 // Byte offsets of moe_forward's intermediates inside the workspace.
 struct Layout {
     size_t ids, w, counts, offsets, perm, inv, scratch, hperm, act, y;
-    size_t hq, hs, aq, as;                 // MX formats: hidden and act, E4M3 codes and E8M0 scales
+    size_t hq, hs, aq, as;                 // 8-bit rows: hidden and act, codes and scales
     size_t done;                           // moe_forward_fused: per-expert and finish counters
     size_t hidden_in, logits_in, out_st;   // staging for moe_forward_host
     size_t total;
@@ -93,8 +107,8 @@ Layout layout(const moe_shape_t *s, bool host) {
     L.perm = take(P * 4);
     L.inv = take(P * 4);
     L.scratch = take(moe::permute_scratch_bytes(static_cast<long long>(P), E));
-    L.hperm = moe::gemm_gathers_in_kernel(static_cast<int>(P), E, s->fmt) ? o : take(P * s->H * 2);
-    const bool mx = is_mx(s->fmt);
+    const bool mx = is_mx(s->fmt), i8 = is_i8(s->fmt), gathers = gathers_in_kernel(s);
+    L.hperm = gathers || i8 ? o : take(P * s->H * 2);
     L.act = mx ? o : take(P * s->I * 2);
     L.y = take(P * s->H * 2);
     L.hq = L.hs = L.aq = L.as = o;
@@ -103,6 +117,14 @@ Layout layout(const moe_shape_t *s, bool host) {
         L.hs = take(static_cast<size_t>(s->T) * s->H / 32);
         L.aq = take(P * s->I);
         L.as = take(P * s->I / 32);
+    }
+    if (i8) {
+        // hidden's int8 rows: one per token, or, when gate/up does not gather, one per pair
+        const size_t rows = gathers ? static_cast<size_t>(s->T) : P;
+        L.hq = take(rows * s->H);
+        L.hs = take(rows * 4);
+        L.aq = take(P * s->I);
+        L.as = take(P * 4);
     }
     L.done = take(moe::fused_counter_words(s->E, s->n_shared) * 4);
     L.hidden_in = L.logits_in = L.out_st = 0;
@@ -162,7 +184,38 @@ moe::MxGemmArgs mx_args(const moe_shape_t *s, const uint8_t *a_q, const uint8_t 
     return m;
 }
 
-moe_status_t forward_device(const moe_bf16_t *hidden, const float *logits, const void *w_gu,
+// The int8 GEMM arguments: token rows a_q with scales a_sf, weight-row scales
+// w_sf, output act or y.
+moe::I8GemmArgs i8_args(const moe_shape_t *s, const int8_t *a_q, const float *a_sf, const int32_t *perm,
+                        const int32_t *offsets, const void *w, const void *w_sf, bool swiglu, moe_bf16_t *out) {
+    moe::I8GemmArgs m;
+    m.base = gemm_args(s, a_q, perm, offsets, w, nullptr, swiglu, out);
+    m.w_sf = static_cast<const float *>(w_sf);
+    m.x_sf = a_sf;
+    return m;
+}
+
+// moe_route_scored's router: what it allows for E experts and top_k slots.
+moe_status_t check_router(const moe_router_t *r, const moe_shape_t *s) {
+    if (!r) return MOE_ERR_INVALID_ARG;
+    if ((r->logits != MOE_LOGITS_FP32 && r->logits != MOE_LOGITS_BF16) ||
+        (r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID) || r->n_group < 1 ||
+        r->topk_group < 1 || r->topk_group > r->n_group || s->E % r->n_group ||
+        (r->group_top != 1 && r->group_top != 2) || (r->renormalize != 0 && r->renormalize != 1) ||
+        !std::isfinite(r->scale))
+        return MOE_ERR_INVALID_ARG;
+    const int size = s->E / r->n_group;
+    if (r->n_group > 1 && r->group_top > size) return MOE_ERR_INVALID_ARG;
+    if (static_cast<long long>(r->topk_group) * size < s->top_k) return MOE_ERR_INVALID_ARG;
+    if (r->n_group > moe::kRouteMaxGroups) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+inline uintptr_t logits_align(const moe_router_t *r) { return r->logits == MOE_LOGITS_BF16 ? 2 : 4; }
+
+// router: null for moe_route's routing of fp32 logits.
+moe_status_t forward_device(const moe_bf16_t *hidden, const void *logits, const float *bias,
+                            const moe_router_t *router, const void *w_gu,
                             const void *w_gu_scales, const void *w_d, const void *w_d_scales,
                             const moe_shape_t *s, moe_bf16_t *out, uint8_t *ws, const Layout &L,
                             cudaStream_t st) {
@@ -180,17 +233,19 @@ moe_status_t forward_device(const moe_bf16_t *hidden, const float *logits, const
     auto *act = reinterpret_cast<uint16_t *>(ws + L.act);
     auto *y = reinterpret_cast<uint16_t *>(ws + L.y);
     // a decode batch with bf16 weights: the whole layer in one persistent kernel
-    if (moe::fused_decode_supported(T, H, s->I, Er, kr, S, s->fmt))
-        return cuda_status(moe::launch_fused_decode(logits, hidden, w_gu, w_d, T, H, s->I, Er, kr, S, ids, w, counts,
+    if (!router && moe::fused_decode_supported(T, H, s->I, Er, kr, S, s->fmt))
+        return cuda_status(moe::launch_fused_decode(static_cast<const float *>(logits), hidden, w_gu, w_d, T, H, s->I, Er, kr, S, ids, w, counts,
                                                     offsets, perm, inv, act, y, out,
                                                     reinterpret_cast<unsigned int *>(ws + L.done), error_flag_ptr(),
                                                     st));
     cudaError_t e;
-    if (moe::route_permute_fusable(T, E, k)) {
-        e = moe::launch_route_permute(logits, T, Er, kr, S, ids, w, counts, offsets, perm, inv, error_flag_ptr(), st);
+    if (!router && moe::route_permute_fusable(T, E, k)) {
+        e = moe::launch_route_permute(static_cast<const float *>(logits), T, Er, kr, S, ids, w, counts, offsets, perm, inv, error_flag_ptr(), st);
         if (e != cudaSuccess) return cuda_status(e);
     } else {
-        if ((e = moe::launch_route(logits, T, Er, kr, S, ids, w, st)) != cudaSuccess) return cuda_status(e);
+        e = router ? moe::launch_route_scored(logits, bias, *router, T, Er, kr, S, ids, w, st)
+                   : moe::launch_route(static_cast<const float *>(logits), T, Er, kr, S, ids, w, st);
+        if (e != cudaSuccess) return cuda_status(e);
         if ((e = moe::launch_permute(ids, P, E, counts, offsets, perm, inv, ws + L.scratch, error_flag_ptr(), st)) !=
             cudaSuccess)
             return cuda_status(e);
@@ -205,6 +260,22 @@ moe_status_t forward_device(const moe_bf16_t *hidden, const float *logits, const
         if (e != cudaSuccess) return cuda_status(e);
         e = moe::launch_grouped_gemm_mxfp8(mx_args(s, aq, as, nullptr, offsets, w_d, w_d_scales, false, nullptr,
                                                    nullptr, y), st);
+        if (e != cudaSuccess) return cuda_status(e);
+        return cuda_status(moe::launch_finalize(y, w, inv, T, H, k, out, error_flag_ptr(), st));
+    }
+    if (is_i8(s->fmt)) {
+        // int8 weights: hidden quantised once per token (with many rows per expert its
+        // rows go straight to their permuted places), act between the two GEMMs
+        auto *hq = reinterpret_cast<int8_t *>(ws + L.hq), *aq = reinterpret_cast<int8_t *>(ws + L.aq);
+        auto *hs = reinterpret_cast<float *>(ws + L.hs), *as = reinterpret_cast<float *>(ws + L.as);
+        const bool gathers = gathers_in_kernel(s);
+        if ((e = moe::launch_i8_quantize(hidden, T, H, hq, hs, gathers ? nullptr : inv, k, st)) != cudaSuccess)
+            return cuda_status(e);
+        e = moe::launch_grouped_gemm_i8(i8_args(s, hq, hs, gathers ? perm : nullptr, offsets, w_gu, w_gu_scales, true,
+                                                act), st);
+        if (e != cudaSuccess) return cuda_status(e);
+        if ((e = moe::launch_i8_quantize(act, P, s->I, aq, as, nullptr, 1, st)) != cudaSuccess) return cuda_status(e);
+        e = moe::launch_grouped_gemm_i8(i8_args(s, aq, as, nullptr, offsets, w_d, w_d_scales, false, y), st);
         if (e != cudaSuccess) return cuda_status(e);
         return cuda_status(moe::launch_finalize(y, w, inv, T, H, k, out, error_flag_ptr(), st));
     }
@@ -301,7 +372,8 @@ moe_status_t forward_host_chunked(const moe_bf16_t *hidden_host, const float *lo
         cs.T = tc;
         const moe_status_t st = forward_device(
             reinterpret_cast<const moe_bf16_t *>(base + L.hidden_in) + t0 * H,
-            reinterpret_cast<const float *>(base + L.logits_in) + t0 * E, w_gu, w_gu_scales, w_d, w_d_scales, &cs,
+            reinterpret_cast<const float *>(base + L.logits_in) + t0 * E, nullptr, nullptr, w_gu, w_gu_scales, w_d,
+            w_d_scales, &cs,
             reinterpret_cast<moe_bf16_t *>(base + L.out_st) + t0 * H, base, layout(&cs, false), s);
         if (st != MOE_OK) return st;
         if (cudaEventRecord(hp->comp_done[c], s) != cudaSuccess ||
@@ -355,6 +427,21 @@ moe_status_t moe_route(const float *logits, const moe_shape_t *shape, int32_t *t
                                          topk_w, static_cast<cudaStream_t>(stream)));
 }
 
+moe_status_t moe_route_scored(const void *logits, const float *bias, const moe_router_t *router,
+                              const moe_shape_t *shape, int32_t *topk_ids, float *topk_w, moe_stream_t stream) {
+    const moe::NvtxRange nvtx("moe_route_scored");
+    moe_status_t st = check_shape(shape);
+    if (st != MOE_OK) return st;
+    if ((st = check_router(router, shape)) != MOE_OK) return st;
+    if (shape->T == 0) return MOE_OK;
+    if (!logits || !topk_ids || !topk_w || !aligned(logits, logits_align(router)) || !aligned(bias, 4) ||
+        !aligned(topk_ids, 4) || !aligned(topk_w, 4))
+        return MOE_ERR_INVALID_ARG;
+    return cuda_status(moe::launch_route_scored(logits, bias, *router, shape->T, shape->E, shape->top_k,
+                                                shape->n_shared, topk_ids, topk_w,
+                                                static_cast<cudaStream_t>(stream)));
+}
+
 moe_status_t moe_permute(const int32_t *topk_ids, const moe_shape_t *shape, int32_t *counts, int32_t *offsets,
                          int32_t *perm, int32_t *inv_perm, const moe_bf16_t *hidden, moe_bf16_t *hidden_perm,
                          void *ws, size_t ws_bytes, moe_stream_t stream) {
@@ -389,7 +476,7 @@ moe_status_t moe_grouped_gemm_swiglu(const moe_bf16_t *a, const int32_t *perm, c
     const moe::NvtxRange nvtx("moe_grouped_gemm_swiglu");
     moe_status_t st = check_shape(shape);
     if (st != MOE_OK) return st;
-    if (is_mx(shape->fmt)) return MOE_ERR_UNSUPPORTED;             // moe_grouped_gemm_swiglu_mx
+    if (is_mx(shape->fmt) || is_i8(shape->fmt)) return MOE_ERR_UNSUPPORTED;   // moe_grouped_gemm_swiglu_mx, _i8
     if (shape->T == 0) return MOE_OK;
     if (!a || !offsets || !act || !aligned(a, 16) || !aligned(act, 16) || !aligned(offsets, 4))
         return MOE_ERR_INVALID_ARG;
@@ -405,7 +492,7 @@ moe_status_t moe_grouped_gemm_down(const moe_bf16_t *act, const int32_t *offsets
     const moe::NvtxRange nvtx("moe_grouped_gemm_down");
     moe_status_t st = check_shape(shape);
     if (st != MOE_OK) return st;
-    if (is_mx(shape->fmt)) return MOE_ERR_UNSUPPORTED;             // moe_grouped_gemm_down_mx
+    if (is_mx(shape->fmt) || is_i8(shape->fmt)) return MOE_ERR_UNSUPPORTED;   // moe_grouped_gemm_down_mx, _i8
     if (shape->T == 0) return MOE_OK;
     if (!act || !offsets || !y || !aligned(act, 16) || !aligned(y, 16) || !aligned(offsets, 4))
         return MOE_ERR_INVALID_ARG;
@@ -438,7 +525,8 @@ int32_t moe_forward_kernel_count(const moe_shape_t *shape) {
         n += 1;                                                       // route + permute in one CTA
     else
         n += 1 + moe::permute_kernel_count(P, E);                     // route; permute in 1, 2 or 3 kernels
-    if (!moe::gemm_gathers_in_kernel(static_cast<int>(P), E, shape->fmt)) n += 1;   // gather
+    if (is_i8(shape->fmt)) n += 2;                                    // int8 quantisation of hidden and of act
+    else if (!gathers_in_kernel(shape)) n += 1;                       // gather
     if (is_mx(shape->fmt)) n += 1;                                    // MX quantisation of hidden
     return n + 3;                                                     // gate/up, down, finalize
 }
@@ -453,7 +541,7 @@ int32_t moe_forward_is_fused(const moe_shape_t *shape) {
 
 int32_t moe_forward_gathers_in_gemm(const moe_shape_t *shape) {
     if (check_shape(shape) != MOE_OK) return -1;
-    return moe::gemm_gathers_in_kernel(shape->T * slots(shape), experts(shape), shape->fmt) ? 1 : 0;
+    return gathers_in_kernel(shape) ? 1 : 0;
 }
 
 moe_status_t moe_forward(const moe_bf16_t *hidden, const float *logits, const void *w_gu,
@@ -471,7 +559,28 @@ moe_status_t moe_forward(const moe_bf16_t *hidden, const float *logits, const vo
     const Layout L = layout(shape, false);
     if (!ws || ws_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
     if (!aligned(ws, 256)) return MOE_ERR_INVALID_ARG;
-    return forward_device(hidden, logits, w_gu, w_gu_scales, w_d, w_d_scales, shape, out,
+    return forward_device(hidden, logits, nullptr, nullptr, w_gu, w_gu_scales, w_d, w_d_scales, shape, out,
+                          static_cast<uint8_t *>(ws), L, static_cast<cudaStream_t>(stream));
+}
+
+moe_status_t moe_forward_scored(const moe_bf16_t *hidden, const void *logits, const float *bias,
+                                const moe_router_t *router, const void *w_gu, const void *w_gu_scales,
+                                const void *w_d, const void *w_d_scales, const moe_shape_t *shape, moe_bf16_t *out,
+                                void *ws, size_t ws_bytes, moe_stream_t stream) {
+    const moe::NvtxRange nvtx("moe_forward_scored");
+    moe_status_t st = check_shape(shape);
+    if (st != MOE_OK) return st;
+    if ((st = check_router(router, shape)) != MOE_OK) return st;
+    if (shape->T == 0) return MOE_OK;
+    if (!hidden || !logits || !out || !aligned(hidden, 16) || !aligned(out, 16) ||
+        !aligned(logits, logits_align(router)) || !aligned(bias, 4))
+        return MOE_ERR_INVALID_ARG;
+    if ((st = check_weights(shape, w_gu, w_gu_scales)) != MOE_OK) return st;
+    if ((st = check_weights(shape, w_d, w_d_scales)) != MOE_OK) return st;
+    const Layout L = layout(shape, false);
+    if (!ws || ws_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    if (!aligned(ws, 256)) return MOE_ERR_INVALID_ARG;
+    return forward_device(hidden, logits, bias, router, w_gu, w_gu_scales, w_d, w_d_scales, shape, out,
                           static_cast<uint8_t *>(ws), L, static_cast<cudaStream_t>(stream));
 }
 
@@ -528,8 +637,8 @@ moe_status_t moe_forward_host(const moe_bf16_t *hidden_host, const float *logits
     if (cudaMemcpyAsync(base + L.logits_in, logits_host, lb, cudaMemcpyHostToDevice, s) != cudaSuccess)
         return MOE_ERR_CUDA;
     st = forward_device(reinterpret_cast<const moe_bf16_t *>(base + L.hidden_in),
-                        reinterpret_cast<const float *>(base + L.logits_in), w_gu, w_gu_scales, w_d, w_d_scales,
-                        shape, reinterpret_cast<moe_bf16_t *>(base + L.out_st), base, L, s);
+                        reinterpret_cast<const float *>(base + L.logits_in), nullptr, nullptr, w_gu, w_gu_scales, w_d,
+                        w_d_scales, shape, reinterpret_cast<moe_bf16_t *>(base + L.out_st), base, L, s);
     if (st != MOE_OK) return st;
     if (cudaMemcpyAsync(out_host, base + L.out_st, hb, cudaMemcpyDeviceToHost, s) != cudaSuccess)
         return MOE_ERR_CUDA;
@@ -579,6 +688,81 @@ moe_status_t moe_grouped_gemm_down_mx(const uint8_t *act_q, const uint8_t *act_s
     if ((st = check_weights(shape, w_d, w_d_scales)) != MOE_OK) return st;
     return cuda_status(moe::launch_grouped_gemm_mxfp8(
         mx_args(shape, act_q, act_scales, nullptr, offsets, w_d, w_d_scales, false, nullptr, nullptr, y),
+        static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_rmsnorm(const moe_bf16_t *x, const moe_bf16_t *residual, const moe_bf16_t *weight, float eps,
+                         int32_t rows, int32_t H, int32_t fmt, moe_bf16_t *residual_out, moe_bf16_t *y, void *q,
+                         void *scales, moe_stream_t stream) {
+    const moe::NvtxRange nvtx("moe_rmsnorm");
+    const bool mx = is_mx(fmt), i8 = is_i8(fmt);
+    if (!mx && !i8 && fmt != MOE_W_BF16 && fmt != MOE_W_INT4_G128) return MOE_ERR_INVALID_ARG;
+    if (rows < 0 || H <= 0 || H % (mx ? 32 : i8 ? 16 : 8) || !(eps > 0.0f) || !std::isfinite(eps))
+        return MOE_ERR_INVALID_ARG;
+    if (H > kMaxRow) return MOE_ERR_UNSUPPORTED;
+    if (rows == 0) return MOE_OK;
+    const bool quantised = mx || i8;
+    if (!x || !weight || (residual == nullptr) != (residual_out == nullptr) || (!quantised && !y) ||
+        (q != nullptr) != quantised || (scales != nullptr) != quantised)
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(residual_out, 16) ||
+        !aligned(y, 16) || !aligned(q, 16) || !aligned(scales, 4))
+        return MOE_ERR_INVALID_ARG;
+    moe::NormArgs n;
+    n.x = x;
+    n.residual = residual;
+    n.weight = weight;
+    n.eps = eps;
+    n.rows = rows;
+    n.H = H;
+    n.residual_out = residual_out;
+    n.y = y;
+    n.q = q;
+    n.scales = scales;
+    n.int8 = i8;
+    return cuda_status(moe::launch_rmsnorm(n, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_i8_quantize(const moe_bf16_t *x, int32_t rows, int32_t K, int8_t *q, float *scales,
+                             moe_stream_t stream) {
+    const moe::NvtxRange nvtx("moe_i8_quantize");
+    if (rows < 0 || K <= 0 || K % 16) return MOE_ERR_INVALID_ARG;
+    if (K > kMaxRow) return MOE_ERR_UNSUPPORTED;
+    if (rows == 0) return MOE_OK;
+    if (!x || !q || !scales || !aligned(x, 16) || !aligned(q, 16) || !aligned(scales, 4)) return MOE_ERR_INVALID_ARG;
+    return cuda_status(moe::launch_i8_quantize(x, rows, K, q, scales, nullptr, 1, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_grouped_gemm_swiglu_i8(const int8_t *a_q, const float *a_scales, const int32_t *perm,
+                                        const int32_t *offsets, const void *w_gu, const void *w_gu_scales,
+                                        const moe_shape_t *shape, moe_bf16_t *act, moe_stream_t stream) {
+    const moe::NvtxRange nvtx("moe_grouped_gemm_swiglu_i8");
+    moe_status_t st = check_shape(shape);
+    if (st != MOE_OK) return st;
+    if (!is_i8(shape->fmt)) return MOE_ERR_INVALID_ARG;
+    if (shape->T == 0) return MOE_OK;
+    if (!a_q || !a_scales || !offsets || !act || !aligned(a_q, 16) || !aligned(a_scales, 4) || !aligned(act, 16) ||
+        !aligned(offsets, 4) || !aligned(perm, 4))
+        return MOE_ERR_INVALID_ARG;
+    if ((st = check_weights(shape, w_gu, w_gu_scales)) != MOE_OK) return st;
+    return cuda_status(moe::launch_grouped_gemm_i8(
+        i8_args(shape, a_q, a_scales, perm, offsets, w_gu, w_gu_scales, true, act), static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_grouped_gemm_down_i8(const int8_t *act_q, const float *act_scales, const int32_t *offsets,
+                                      const void *w_d, const void *w_d_scales, const moe_shape_t *shape,
+                                      moe_bf16_t *y, moe_stream_t stream) {
+    const moe::NvtxRange nvtx("moe_grouped_gemm_down_i8");
+    moe_status_t st = check_shape(shape);
+    if (st != MOE_OK) return st;
+    if (!is_i8(shape->fmt)) return MOE_ERR_INVALID_ARG;
+    if (shape->T == 0) return MOE_OK;
+    if (!act_q || !act_scales || !offsets || !y || !aligned(act_q, 16) || !aligned(act_scales, 4) ||
+        !aligned(y, 16) || !aligned(offsets, 4))
+        return MOE_ERR_INVALID_ARG;
+    if ((st = check_weights(shape, w_d, w_d_scales)) != MOE_OK) return st;
+    return cuda_status(moe::launch_grouped_gemm_i8(
+        i8_args(shape, act_q, act_scales, nullptr, offsets, w_d, w_d_scales, false, y),
         static_cast<cudaStream_t>(stream)));
 }
 

@@ -438,6 +438,30 @@ __device__ __forceinline__ void umma_mxf8_ss(uint32_t d_tmem, uint64_t a_desc, u
         : "memory");
 }
 
+// --- int8 operands, int32 accumulator (kind::i8) -------------------------------
+
+// Instruction descriptor, kind::i8: signed 8-bit A and B (both K-major), int32
+// D, shape M x N (M = 128: N = 16 or a multiple of 16 in [32, 256]; M = 256
+// across a CTA pair: a multiple of 32 in [32, 256]).
+__host__ __device__ __forceinline__ uint32_t idesc_i8_i32(int M, int N) {
+    return (2u << 4)                                        // D format: s32
+           | (1u << 7)                                      // A format: s8
+           | (1u << 10)                                     // B format: s8
+           | (static_cast<uint32_t>(N >> 3) << 17)          // N >> 3
+           | (static_cast<uint32_t>(M >> 4) << 24);         // M >> 4
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T, K = 32 per instruction, one CTA.
+__device__ __forceinline__ void umma_i8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // ----------------------------------------------------------------- numerics --
 
 __device__ __forceinline__ float bf16_bits_to_float(uint32_t b16) {

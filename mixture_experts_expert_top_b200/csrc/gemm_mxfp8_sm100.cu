@@ -32,10 +32,9 @@
 // so a stage holds the same K = 128 per 128-byte row as for E4M3 while HBM
 // carries half the bytes. Everything else (scale factors, epilogues) is the
 // MXFP8 kernel's.
-#include <cuda_fp8.h>
-
 #include "gemm_common.cuh"
 #include "launch_util.cuh"
+#include "mx_dev.cuh"
 
 namespace moe {
 namespace {
@@ -45,22 +44,6 @@ using namespace gemm;
 constexpr int kMxBK = 128;                      // K elements (bytes) per stage and operand row
 constexpr int kMxTileA = kBM * kMxBK;           // 16 KB
 constexpr int kSfBlock = 512;                   // scale factors of 128 rows x 4 K blocks
-
-// E4M3 code of x (round to nearest even, saturate to +-448).
-__device__ __forceinline__ uint8_t e4m3_rn_sat(float x) {
-    return static_cast<uint8_t>(__nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3));
-}
-
-// Block exponent of an MX block from the bits of its max |x| (a non-negative
-// float): floor(log2 amax) - 8, clamped to [-127, 127]; -127 for amax = 0.
-__device__ __forceinline__ int mx_block_exponent(uint32_t amax_bits) {
-    if (amax_bits == 0) return -127;
-    const int biased = static_cast<int>(amax_bits >> 23);       // 0 for a subnormal max
-    return max(biased - 127 - 8, -127);
-}
-
-// 2^-e as an fp32 (normal for every e the exponent rule gives).
-__device__ __forceinline__ float mx_inverse_scale(int e) { return __uint_as_float(static_cast<uint32_t>(127 - e) << 23); }
 
 // MX quantisation of bf16 rows [rows, K] (K % 32 == 0): one thread per 8
 // elements, 4 consecutive lanes per 32-element block. Whole warps step

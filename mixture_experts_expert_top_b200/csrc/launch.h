@@ -44,6 +44,31 @@ cudaError_t launch_bounded_wait_selftest(unsigned long long limit_ns, int *err, 
 cudaError_t launch_route(const float *logits, int T, int E, int k, int n_shared, int32_t *ids, float *w,
                          cudaStream_t s);
 
+// ---- route_scored.cu
+constexpr int kRouteMaxGroups = 32;     // a group per lane
+// Scored routing (softmax or sigmoid, selection bias, groups): ids/w rows as
+// launch_route's. logits fp32, or bf16 when router.logits is
+// MOE_LOGITS_BF16; bias [E] fp32 or null.
+cudaError_t launch_route_scored(const void *logits, const float *bias, const moe_router_t &router, int T, int E, int k,
+                                int n_shared, int32_t *ids, float *w, cudaStream_t s);
+
+// ---- norm.cu
+struct NormArgs {
+    const uint16_t *x, *residual, *weight;  // [rows, H], [rows, H] or null, [H]: bf16
+    float eps;
+    int rows, H;                            // H % 8 == 0, H <= 32768 (MXFP8: H % 32 == 0)
+    uint16_t *residual_out, *y;             // [rows, H] bf16, each may be null
+    void *q, *scales;                       // 8-bit rows or null: E4M3 + E8M0 [rows, H/32], or int8 + fp32 [rows]
+    bool int8;
+};
+cudaError_t launch_rmsnorm(const NormArgs &n, cudaStream_t s);
+// bf16 rows [rows, K] -> int8 [rows, K] and fp32 scales [rows] (K % 8 == 0,
+// K <= 32768). With inv_perm [rows * slots]: row t goes to the rows
+// inv_perm[t * slots + j] of q and scales [rows * slots] instead (the
+// layer's gather; entries out of range are skipped).
+cudaError_t launch_i8_quantize(const uint16_t *x, int rows, int K, int8_t *q, float *scales, const int32_t *inv_perm,
+                               int slots, cudaStream_t s);
+
 // ---- route_permute.cu
 // Routing and bucketing of a small batch by one CTA (same outputs as
 // launch_route followed by launch_permute).
@@ -121,6 +146,17 @@ struct MxGemmArgs {
     uint8_t *out_sf;            // gate/up: act E8M0 [P, I/32]
 };
 cudaError_t launch_grouped_gemm_mxfp8(const MxGemmArgs &g, cudaStream_t s);
+// ---- gemm_i8_sm100.cu: int8 weights with an fp32 scale per output channel
+// times int8 token rows with an fp32 scale per row, int32 accumulators.
+struct I8GemmArgs {
+    GemmArgs base;              // base.a: int8 token rows; base.out: act or y as bf16
+    const float *w_sf;          // [E * w_rows] weight-row scales
+    const float *x_sf;          // [rows of base.a] token-row scales
+};
+cudaError_t launch_grouped_gemm_i8(const I8GemmArgs &g, cudaStream_t s);
+// True when the layer's int8 gate/up GEMM should read the token rows through
+// perm itself (few rows per expert).
+bool gemm_i8_gathers_in_kernel(int P, int E);
 // ---- fused_decode_sm100.cu: the whole bf16 layer for a decode batch in one
 // persistent kernel (T <= 64, k + S <= 16, E + S <= 256). done:
 // fused_counter_words(E, S) counters of the workspace, zeroed on the stream
