@@ -211,26 +211,35 @@ def _p(t, *dtypes) -> Optional[int]:
     return t.data_ptr()
 
 
-def _pd(t, n: int, *dtypes) -> Optional[int]:
-    """_p of a tensor of at least n elements on the current CUDA device (None
-    for None): a host tensor, a tensor of another device or a short one is
-    refused before the library is called. An address (int) passes as it is."""
-    if t is None or isinstance(t, int):
+def _pd(t, n: int, dtype, dev: int) -> Optional[int]:
+    """_p of a contiguous tensor of this dtype with at least n elements on CUDA
+    device dev (None for None): a host tensor, a tensor of another device or a
+    short one is refused before the library is called. An address (int) passes
+    as it is."""
+    if t is None or t.__class__ is int:
         return t
-    if t.dtype not in dtypes:
-        raise TypeError(f"libmoe_b200: expected a tensor of {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.dtype is dtype and t.numel() >= n and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype is not dtype:
+        raise TypeError(f"libmoe_b200: expected a tensor of {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError("tensors passed to libmoe_b200 must be contiguous")
     if t.numel() < n:
         raise ValueError(f"libmoe_b200: expected at least {n} elements, got a tensor of shape {tuple(t.shape)}")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"libmoe_b200: expected a tensor on the current CUDA device, got one on {t.device}")
-    return t.data_ptr()
+    raise ValueError(f"libmoe_b200: expected a tensor on the current CUDA device, got one on {t.device}")
+
+
+def _dev() -> int:
+    """Index of the current CUDA device (-2 while this process has not used CUDA:
+    then no tensor is on one)."""
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
 
 
 def _s(stream) -> Optional[int]:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the handle of torch.cuda.current_stream() without building the Stream object,
+        # which takes longer (3.3 us) than a kernel's launch
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -268,23 +277,23 @@ def moe_route(logits, shape, topk_ids, topk_w, stream=None) -> None:
 
 
 def moe_route_scored(logits, bias, router: Router, shape, topk_ids, topk_w, stream=None) -> None:
-    sh = _shape(shape)
-    T, E, slots = sh.T, sh.E, sh.T * sh.slots
-    _check(lib().moe_route_scored(_pd(logits, T * E, BF16 if router.logits == 1 else F32), _pd(bias, E, F32),
-                                  ctypes.byref(router), ctypes.byref(sh), _pd(topk_ids, slots, I32),
-                                  _pd(topk_w, slots, F32), _s(stream)),
+    sh, d = _shape(shape), _dev()
+    T, E = sh.T, sh.E
+    n = T * sh.slots
+    _check(lib().moe_route_scored(_pd(logits, T * E, BF16 if router.logits else F32, d), _pd(bias, E, F32, d),
+                                  router, sh, _pd(topk_ids, n, I32, d), _pd(topk_w, n, F32, d), _s(stream)),
            "moe_route_scored")
 
 
 def moe_rmsnorm(x, residual, weight, eps: float, rows: int, H: int, fmt, residual_out, y, q=None, scales=None,
                 stream=None) -> None:
-    n = rows * H
+    n, d = rows * H, _dev()
     if fmt == FMT_INT8:
-        q_p, s_p = _pd(q, n, I8), _pd(scales, rows, F32)
+        q_p, s_p = _pd(q, n, I8, d), _pd(scales, rows, F32, d)
     else:
-        q_p, s_p = _pd(q, n, U8), _pd(scales, n // 32, U8)
-    _check(lib().moe_rmsnorm(_pd(x, n, BF16), _pd(residual, n, BF16), _pd(weight, H, BF16), float(eps), rows, H, fmt,
-                             _pd(residual_out, n, BF16), _pd(y, n, BF16), q_p, s_p, _s(stream)),
+        q_p, s_p = _pd(q, n, U8, d), _pd(scales, n // 32, U8, d)
+    _check(lib().moe_rmsnorm(_pd(x, n, BF16, d), _pd(residual, n, BF16, d), _pd(weight, H, BF16, d), eps, rows, H, fmt,
+                             _pd(residual_out, n, BF16, d), _pd(y, n, BF16, d), q_p, s_p, _s(stream)),
            "moe_rmsnorm")
 
 
@@ -371,51 +380,51 @@ def moe_grouped_gemm_down_mx(act_q, act_scales, offsets, w_d, w_d_scales, shape,
 
 
 def moe_i8_quantize(x, rows: int, K: int, q, scales, stream=None) -> None:
-    _check(lib().moe_i8_quantize(_pd(x, rows * K, BF16), rows, K, _pd(q, rows * K, I8), _pd(scales, rows, F32),
+    n, d = rows * K, _dev()
+    _check(lib().moe_i8_quantize(_pd(x, n, BF16, d), rows, K, _pd(q, n, I8, d), _pd(scales, rows, F32, d),
                                  _s(stream)),
            "moe_i8_quantize")
 
 
 def moe_grouped_gemm_swiglu_i8(a_q, a_scales, perm, offsets, w_gu, w_gu_scales, shape, act, stream=None) -> None:
-    sh = _shape(shape)
-    P, E = sh.T * sh.slots, sh.experts
+    sh, d = _shape(shape), _dev()
+    P, E, H, I = sh.T * sh.slots, sh.experts, sh.H, sh.I
     rows = P if perm is None else sh.T
-    _check(lib().moe_grouped_gemm_swiglu_i8(_pd(a_q, rows * sh.H, I8), _pd(a_scales, rows, F32), _pd(perm, P, I32),
-                                            _pd(offsets, E + 1, I32), _pd(w_gu, E * 2 * sh.I * sh.H, I8),
-                                            _pd(w_gu_scales, E * 2 * sh.I, F32), ctypes.byref(sh),
-                                            _pd(act, P * sh.I, BF16), _s(stream)),
+    _check(lib().moe_grouped_gemm_swiglu_i8(_pd(a_q, rows * H, I8, d), _pd(a_scales, rows, F32, d),
+                                            _pd(perm, P, I32, d), _pd(offsets, E + 1, I32, d),
+                                            _pd(w_gu, E * 2 * I * H, I8, d), _pd(w_gu_scales, E * 2 * I, F32, d), sh,
+                                            _pd(act, P * I, BF16, d), _s(stream)),
            "moe_grouped_gemm_swiglu_i8")
 
 
 def moe_grouped_gemm_down_i8(act_q, act_scales, offsets, w_d, w_d_scales, shape, y, stream=None) -> None:
-    sh = _shape(shape)
-    P, E = sh.T * sh.slots, sh.experts
-    _check(lib().moe_grouped_gemm_down_i8(_pd(act_q, P * sh.I, I8), _pd(act_scales, P, F32), _pd(offsets, E + 1, I32),
-                                          _pd(w_d, E * sh.H * sh.I, I8), _pd(w_d_scales, E * sh.H, F32),
-                                          ctypes.byref(sh), _pd(y, P * sh.H, BF16), _s(stream)),
+    sh, d = _shape(shape), _dev()
+    P, E, H, I = sh.T * sh.slots, sh.experts, sh.H, sh.I
+    _check(lib().moe_grouped_gemm_down_i8(_pd(act_q, P * I, I8, d), _pd(act_scales, P, F32, d),
+                                          _pd(offsets, E + 1, I32, d), _pd(w_d, E * H * I, I8, d),
+                                          _pd(w_d_scales, E * H, F32, d), sh, _pd(y, P * H, BF16, d), _s(stream)),
            "moe_grouped_gemm_down_i8")
 
 
 def moe_forward_scored(hidden, logits, bias, router: Router, w_gu, w_gu_scales, w_d, w_d_scales, shape, out, ws,
                        stream=None) -> None:
-    sh = _shape(shape)
+    sh, d = _shape(shape), _dev()
     T, H, I, E = sh.T, sh.H, sh.I, sh.experts
-    # bytes and scales per weight row of K elements
-    row = {FMT_BF16: (lambda K: K, lambda K: 0, (BF16,), (BF16,)),
-           FMT_INT4_G128: (lambda K: K // 2, lambda K: K // 128, (U8,), (BF16,)),
-           FMT_MXFP8: (lambda K: K, lambda K: K // 32, (U8,), (U8,)),
-           FMT_MXFP4: (lambda K: K // 2, lambda K: K // 32, (U8,), (U8,)),
-           FMT_INT8: (lambda K: K, lambda K: 1, (I8,), (F32,))}
+    # per weight row of K elements: codes and scales, and their types
+    row = {FMT_BF16: (lambda K: K, lambda K: 0, BF16, BF16),
+           FMT_INT4_G128: (lambda K: K // 2, lambda K: K // 128, U8, BF16),
+           FMT_MXFP8: (lambda K: K, lambda K: K // 32, U8, U8),
+           FMT_MXFP4: (lambda K: K // 2, lambda K: K // 32, U8, U8),
+           FMT_INT8: (lambda K: K, lambda K: 1, I8, F32)}
     if sh.fmt not in row:
         raise MoeError(1, "moe_forward_scored")
     codes, scales, w_dt, s_dt = row[sh.fmt]
     nbytes = ws.numel() * ws.element_size()
-    _check(lib().moe_forward_scored(_pd(hidden, T * H, BF16),
-                                    _pd(logits, T * sh.E, BF16 if router.logits == 1 else F32), _pd(bias, sh.E, F32),
-                                    ctypes.byref(router), _pd(w_gu, E * 2 * I * codes(H), *w_dt),
-                                    _pd(w_gu_scales, E * 2 * I * scales(H), *s_dt), _pd(w_d, E * H * codes(I), *w_dt),
-                                    _pd(w_d_scales, E * H * scales(I), *s_dt), ctypes.byref(sh),
-                                    _pd(out, T * H, BF16), _pd(ws, 0, ws.dtype), nbytes, _s(stream)),
+    _check(lib().moe_forward_scored(_pd(hidden, T * H, BF16, d), _pd(logits, T * sh.E, BF16 if router.logits else F32, d),
+                                    _pd(bias, sh.E, F32, d), router, _pd(w_gu, E * 2 * I * codes(H), w_dt, d),
+                                    _pd(w_gu_scales, E * 2 * I * scales(H), s_dt, d),
+                                    _pd(w_d, E * H * codes(I), w_dt, d), _pd(w_d_scales, E * H * scales(I), s_dt, d),
+                                    sh, _pd(out, T * H, BF16, d), _pd(ws, 0, ws.dtype, d), nbytes, _s(stream)),
            "moe_forward_scored")
 
 
