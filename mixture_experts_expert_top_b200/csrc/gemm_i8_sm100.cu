@@ -15,7 +15,7 @@
 // 128-byte swizzled row per operand row): four MMAs of K = 32 per accumulator.
 // K need only be a multiple of 16: TMA fills the rest of the last stage with
 // zeros. The scales are applied in the epilogue.
-#include "gemm_common.cuh"
+#include "gemm_i8_common.cuh"
 #include "launch_util.cuh"
 
 namespace moe {
@@ -23,7 +23,6 @@ namespace {
 
 using namespace gemm;
 
-constexpr int kI8BK = 128;                      // K elements (bytes) per stage and operand row
 constexpr int kI8TileA = kBM * kI8BK;           // 16 KB
 
 template <int BN, int STAGES, bool SWIGLU>
@@ -44,12 +43,6 @@ struct I8Cfg {
     static_assert(kTmemUsed <= 512, "TMEM holds 512 32-bit columns");
     static_assert(BN % kBoxN == 0 && BN <= 128, "BN");
     static_assert(kSmemBytes + 64 <= kSmemLimit, "shared memory");
-};
-
-struct I8Params {
-    Params p;
-    const float *w_sf;          // [E * w_rows]
-    const float *x_sf;          // [x_rows]
 };
 
 template <int BN, int STAGES, bool SWIGLU>
@@ -218,10 +211,8 @@ grouped_gemm_i8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
                     const int n = c0 + j;
                     const float sx = __shfl_sync(0xffffffffu, sx_l, j);
                     if (f_ok && n < ti.valid) {
-                        float v = static_cast<float>(static_cast<int>(g[j])) * sg * sx;
-                        if (SWIGLU) v = v / (1.0f + expf(-v)) * (static_cast<float>(static_cast<int>(u[j])) * su * sx);
                         p.out[static_cast<size_t>(ti.row0 + n) * p.m_out + f] =
-                            __bfloat16_as_ushort(__float2bfloat16_rn(v));
+                            SWIGLU ? i8_act(i8_scaled(g[j], sg, sx), i8_scaled(u[j], su, sx)) : i8_down(g[j], sg, sx);
                     }
                 }
             }
@@ -259,11 +250,7 @@ cudaError_t run_i8(const I8GemmArgs &g, cudaStream_t s) {
     if (st != cudaSuccess) return st;
     const int grid = grid_for(g.base, BN);
     if (grid <= 0) return cudaSuccess;
-    I8Params ip;
-    ip.p = make_params(g.base, BN);
-    ip.w_sf = g.w_sf;
-    ip.x_sf = g.x_sf;
-    return launch_pdl(kern, dim3(grid), dim3(C::kThreads), C::kSmemBytes, s, ta, tb, ip);
+    return launch_pdl(kern, dim3(grid), dim3(C::kThreads), C::kSmemBytes, s, ta, tb, make_i8_params(g, BN));
 }
 
 }  // namespace
@@ -273,6 +260,7 @@ bool gemm_i8_gathers_in_kernel(int P, int E) { return static_cast<double>(P) / E
 cudaError_t launch_grouped_gemm_i8(const I8GemmArgs &g, cudaStream_t s) {
     if (g.base.P == 0) return cudaSuccess;
     const double avg = static_cast<double>(g.base.P) / g.base.E;
+    if (!g.base.perm && avg > 48) return launch_grouped_gemm_i8_pair(g, s);
     if (g.base.swiglu) {
         if (avg <= 24) return run_i8<32, 5, true>(g, s);
         if (avg <= 48) return run_i8<64, 5, true>(g, s);

@@ -154,6 +154,9 @@ struct I8GemmArgs {
     const float *x_sf;          // [rows of base.a] token-row scales
 };
 cudaError_t launch_grouped_gemm_i8(const I8GemmArgs &g, cudaStream_t s);
+// ---- gemm_i8_pair_sm100.cu: the same for many tokens per expert (permuted
+// rows, no perm), weights on M across a CTA pair
+cudaError_t launch_grouped_gemm_i8_pair(const I8GemmArgs &g, cudaStream_t s);
 // True when the layer's int8 gate/up GEMM should read the token rows through
 // perm itself (few rows per expert).
 bool gemm_i8_gathers_in_kernel(int P, int E);
