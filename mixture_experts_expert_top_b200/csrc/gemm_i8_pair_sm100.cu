@@ -11,17 +11,19 @@
 //  - B tile = up to 256 token rows of one expert; N is the tile's rows rounded
 //    up to 32 (kind::i8 across a pair takes multiples of 32). The non-leading
 //    CTA loads its rows N/2 into the tile.
-//  - gate/up: CTA r holds the gate rows of features fb*128 + 64r + [0, 64) in
-//    its A rows 0-63 and the up rows of the same features in rows 64-127; the
-//    warps of matching gate and up lanes swap halves of each 32-token chunk
-//    through shared memory and form act for 16 tokens each.
+//  - gate/up: CTA r holds features fb*128 + 64r + [0, 64), its A rows
+//    alternating 16 gate rows and the 16 up rows of the same features (one
+//    5-D TMA box), so that a warp's 32 TMEM lanes hold both factors of its 16
+//    features and no values pass between warps.
 //  - down: CTA r holds output features fb*256 + 128r + [0, 128).
+//  - Epilogue per 32 tokens: tcgen05.ld in MMA-fragment layout (16 lanes x
+//    256 bits), scales, bf16 pairs, stmatrix.trans into rows of tokens, 16-byte
+//    stores. A thread per feature with 2-byte stores (each row a partial
+//    line) took 60 us of the 232 us of the gate/up case below.
 //  - Warp 0 loads (both CTAs), warp 1 issues the MMAs (leading CTA) and owns
 //    TMEM, warps 2-9 run the epilogue over a double-buffered 2 x 256-column
 //    int32 accumulator.
-// Every mbarrier wait is bounded; the named-barrier hand-off between epilogue
-// warps is entered only after a bounded wait succeeded, and both warps of a
-// pair take the same number of steps.
+// Every mbarrier wait is bounded.
 #include "gemm_i8_common.cuh"
 #include "launch_util.cuh"
 
@@ -38,29 +40,21 @@ constexpr int kTileB = (kTokBlock / 2) * kI8BK;      // 16 KB: up to 128 token r
 constexpr int kStage = kTileA + kTileB;              // 32 KB
 constexpr int kAccCols = kTokBlock;                  // int32 accumulator columns per buffer
 constexpr int kEpiWarps = 8;
-constexpr int kPairXchgBytes = 2 * 2 * 16 * 32 * 4;  // one warp pair's gate/up hand-off: 2 buffers x 2 x 16 x 32 fp32
-constexpr int kScaleBytes = kEpiWarps * 2 * 32 * 4;  // token scales of a chunk: per warp, two buffers
+constexpr int kScaleBytes = kEpiWarps * (kTokBlock / 2) * 4;     // token scales of each warp's half tile
 
 template <bool SWIGLU, int STAGES>
 struct I8PairCfg {
     static constexpr int kThreads = 64 + 32 * kEpiWarps;
-    static constexpr int kXchgBytes = SWIGLU ? 4 * kPairXchgBytes : 0;
+    // one warp's staging of 32 token rows: 16 or 32 features and 16 bytes that
+    // keep the eight rows of a stmatrix on different banks
+    static constexpr int kRowBytes = SWIGLU ? 48 : 80;
+    static constexpr int kOutBytes = kEpiWarps * 32 * kRowBytes;
     static constexpr int kRingBytes = STAGES * kStage;
     static constexpr int kNumBars = 2 * STAGES + 2 + 2 + 1;
     static constexpr int kSmemBytes =
-        1024 + kRingBytes + kXchgBytes + kScaleBytes + 8 * kNumBars + 64 + 2 * (kMaxExperts + 1) * 4;
+        1024 + kRingBytes + kOutBytes + kScaleBytes + 8 * kNumBars + 64 + 2 * (kMaxExperts + 1) * 4;
     static_assert(kSmemBytes + 64 <= kSmemLimit, "shared memory");
 };
-
-// Named barriers of the gate/up epilogue (barrier 0 is __syncthreads): per
-// warp pair pq (0-3), "go" carries the gate warp's decision for the tile,
-// "xchg" separates the writes and reads of one chunk's hand-off buffer.
-__device__ __forceinline__ int bar_go(int pq) { return 1 + pq; }
-__device__ __forceinline__ int bar_xchg(int pq) { return 5 + pq; }
-
-__device__ __forceinline__ void named_bar_sync(int id, int nthreads) {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
-}
 
 // decode_tile's row count rounded up to 32.
 __device__ __forceinline__ TileInfo pair_tile(int tile, const int *pre, const int *off, int E, int MB) {
@@ -79,9 +73,9 @@ grouped_gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __gri
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *ring = smem;                                    // STAGES x [A own 128 rows | B own rows]
-    float *xchg = reinterpret_cast<float *>(ring + C::kRingBytes);   // gate/up hand-off buffers
-    float *scale_s = reinterpret_cast<float *>(ring + C::kRingBytes + C::kXchgBytes);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(ring + C::kRingBytes + C::kXchgBytes + kScaleBytes);
+    uint8_t *out_s = ring + C::kRingBytes;                   // per epilogue warp: 32 token rows
+    float *scale_s = reinterpret_cast<float *>(out_s + C::kOutBytes);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(out_s + C::kOutBytes + kScaleBytes);
     uint64_t *full_bar = bars;                               // used in the leading CTA: both CTAs' bytes
     uint64_t *empty_bar = full_bar + STAGES;                 // each CTA's own (MMA commit to both)
     uint64_t *tfull_bar = empty_bar + STAGES;                // each CTA's own (MMA commit to both)
@@ -89,7 +83,6 @@ grouped_gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __gri
     uint64_t *drain_bar = tempty_bar + 2;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain_bar + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
-    volatile int *go_flag = reinterpret_cast<volatile int *>(tmem_holder + 2);     // [4]
     int *off_s = reinterpret_cast<int *>(tmem_holder + 16);
     int *pre_s = off_s + (kMaxExperts + 1);
 
@@ -144,17 +137,17 @@ grouped_gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __gri
                 const int half = ti.n_mma / 2;                       // token rows from each CTA
                 const uint32_t tx = 2u * kStage;
                 const int b_row = ti.row0 + rank * half;             // the non-leading CTA's shift
-                // this CTA's A rows: 64 gate and the matching 64 up rows, or 128 rows
-                const int r0 = SWIGLU ? ti.e * p.w_rows + ti.mb * 128 + 64 * rank
-                                      : ti.e * p.w_rows + ti.mb * 256 + 128 * rank;
                 for (int kb = 0; kb < KB; ++kb) {
                     ok = mbar_wait(&empty_bar[stage], phase ^ 1, abort_flag, p.err, 128);
                     if (!ok) break;
                     const uint32_t full_leader = cluster_map(smem_u32(&full_bar[stage]), 0);
                     uint8_t *st = ring + stage * kStage;
                     if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], tx);
-                    tma_load_2d_pair(st, &tmA, full_leader, kb * kI8BK, r0, pol);
-                    if (SWIGLU) tma_load_2d_pair(st + kTileA / 2, &tmA, full_leader, kb * kI8BK, r0 + p.m_out, pol);
+                    if (SWIGLU)
+                        tma_load_5d_pair(st, &tmA, full_leader, kb * kI8BK, 0, 0, ti.mb * 8 + 4 * rank, ti.e, pol);
+                    else
+                        tma_load_2d_pair(st, &tmA, full_leader, kb * kI8BK, ti.e * p.w_rows + ti.mb * 256 + 128 * rank,
+                                         pol);
                     tma_load_2d_pair(st + kTileA, &tmB, full_leader, kb * kI8BK, b_row, pol);
                     if (++stage == STAGES) { stage = 0; phase ^= 1; }
                 }
@@ -200,15 +193,18 @@ grouped_gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __gri
         // ====================== warps 2-9: epilogue (both CTAs) =================
         const int q = warp & 3;                              // TMEM lane quarter of this warp
         const int h = (warp - 2) >> 2;                       // column half: warps 2-5 first, 6-9 second
-        const bool gate_warp = q < 2;                        // gate/up: which rows this warp's lanes hold
-        const int pq = (q & 1) + 2 * h;                      // gate/up: warp pair index
+        constexpr int kFeat = SWIGLU ? 16 : 32;              // features of a warp
+        constexpr int kPieces = kFeat / 8;                   // 16-byte pieces of its token rows
         const uint32_t tempty_leader0 = cluster_map(smem_u32(&tempty_bar[0]), 0);
         const uint32_t tempty_leader1 = cluster_map(smem_u32(&tempty_bar[1]), 0);
-        float *xb = xchg + pq * (kPairXchgBytes / 4);        // [buffer][giver: gate, up][16 tokens][32 lanes]
-        float *sx_w = scale_s + (warp - 2) * 64;             // [buffer][32 tokens]
-        const int f_in_tile = SWIGLU ? 64 * rank + 32 * (q & 1) + lane : 128 * rank + 32 * q + lane;
+        uint8_t *rows_s = out_s + (warp - 2) * 32 * C::kRowBytes;
+        float *sx_s = scale_s + (warp - 2) * (kTokBlock / 2);
+        // this lane's row address of a stmatrix: matrix lane / 8 is 8 features (down) or,
+        // gate/up, 8 features of token group lane / 16
+        const uint32_t st_addr = smem_u32(rows_s) + (SWIGLU ? ((lane >> 4) * 8 + (lane & 7)) * C::kRowBytes + ((lane >> 3) & 1) * 16
+                                                            : (lane & 7) * C::kRowBytes + (lane >> 3) * 16);
         int buf = 0;
-        uint32_t bphase = 0, xbuf = 0;
+        uint32_t bphase = 0;
         // TMEM accumulator buffer handed back to the MMA issuer once this
         // warp's last tcgen05.ld of the tile has completed. The arrive orders
         // only those loads, so it is relaxed: a release would first wait for
@@ -220,97 +216,88 @@ grouped_gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __gri
         };
         for (int tile = first_tile; tile < total_tiles; tile += tile_step) {
             const TileInfo ti = pair_tile(tile, pre_s, off_s, E, MB);
-            const int f = ti.mb * kFeatPerTile + f_in_tile;
-            const bool f_ok = f < p.m_out;
-            const size_t w_row = static_cast<size_t>(ti.e) * p.w_rows + f;
-            // the scale of the accumulator row in this thread's TMEM lane (gate/up:
-            // a gate row in a gate warp, the matching up row in an up warp)
-            const float sw = f_ok ? __ldg(ip.w_sf + w_row + (SWIGLU && !gate_warp ? p.m_out : 0)) : 0.f;
-            if (!SWIGLU || gate_warp) {
-                const bool ok =
-                    __shfl_sync(0xffffffffu, mbar_wait(&tfull_bar[buf], bphase, abort_flag, p.err, 512), 0);
-                if (!SWIGLU && !ok) break;
-                // gate/up: one decision for the warp pair (the barriers below are collective)
-                if (SWIGLU && lane == 0) go_flag[pq] = ok ? 1 : 0;
-            }
-            if (SWIGLU) {
-                named_bar_sync(bar_go(pq), 64);
-                if (!go_flag[pq]) break;
-                // the phase has completed (the gate warp saw it): this returns at
-                // once and orders this warp's TMEM reads after the MMAs
-                if (!gate_warp) mbar_wait(&tfull_bar[buf], bphase, abort_flag, p.err, 512);
-            }
-            tc_fence_after_sync();
-            // this half's columns: chunks [c_lo, c_hi) of 32
+            // this half's columns: chunks [c_lo, c_hi) of 32 tokens
             const int nch = (ti.valid + 31) >> 5;
             const int split = (nch + 1) >> 1;
             const int c_lo = h ? split : 0, c_hi = h ? nch : split;
+            const int f0 = SWIGLU ? ti.mb * 128 + 64 * rank + 16 * q : ti.mb * 256 + 128 * rank + 32 * q;
+            // weight scales of this thread's accumulator rows lane / 4 + 8 i (gate/up:
+            // i = 0, 1 gate, 2, 3 the matching up rows)
+            float sw[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int f = f0 + (lane >> 2) + 8 * (SWIGLU ? i & 1 : i);
+                const size_t row = static_cast<size_t>(ti.e) * p.w_rows + f + (SWIGLU && i >= 2 ? p.m_out : 0);
+                sw[i] = f < p.m_out ? __ldg(ip.w_sf + row) : 0.f;
+            }
+            // token scales of this half, kept in shared memory for the tile
+            for (int c = c_lo; c < c_hi; ++c) {
+                const int n = 32 * c + lane;
+                sx_s[n - 32 * c_lo] = n < ti.valid ? __ldg(ip.x_sf + ti.row0 + n) : 0.f;
+            }
+            __syncwarp();
+            if (!__shfl_sync(0xffffffffu, mbar_wait(&tfull_bar[buf], bphase, abort_flag, p.err, 512), 0)) break;
+            tc_fence_after_sync();
             if (c_lo >= c_hi) {
                 release();
                 if (++buf == 2) { buf = 0; bphase ^= 1; }
                 continue;
             }
             const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kAccCols;
-            uint16_t *col = p.out + static_cast<size_t>(ti.row0) * p.m_out + f;
-            // the chunk's token scales, one per lane, into this warp's buffer
-            auto scales = [&](int c0) {
-                sx_w[xbuf * 32 + lane] = c0 + lane < ti.valid ? __ldg(ip.x_sf + ti.row0 + c0 + lane) : 0.f;
-                __syncwarp();
+            auto load = [&](uint32_t (&a)[16], uint32_t (&b)[16], int c) {
+                tmem_ld_16x256b_x4(tb + 32 * c, a);
+                tmem_ld_16x256b_x4(tb + (16u << 16) + 32 * c, b);
             };
-            auto chunk = [&](const uint32_t (&v)[32], int c0) {
-                scales(c0);
-                const float *sx = sx_w + xbuf * 32;
-                if constexpr (!SWIGLU) {
-                    if (f_ok) {
-                        uint16_t *dst = col + static_cast<size_t>(c0) * p.m_out;
-                        const int n = min(32, ti.valid - c0);
+            auto chunk = [&](const uint32_t (&a)[16], const uint32_t (&b)[16], int c) {
+                const float *sx = sx_s + 32 * (c - c_lo) + 2 * (lane & 3);
+                uint32_t lo[4], hi[4];                       // gate/up: features 0-7, 8-15 of each token group
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            if (j < n) *dst = i8_down(v[j], sw, sx[j]);
-                            dst += p.m_out;
-                        }
+                for (int g = 0; g < 4; ++g) {
+                    const float2 s = *reinterpret_cast<const float2 *>(sx + 8 * g);
+                    float v[8];                              // [row lane / 4 + 8 i][token 0, 1]
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t *r = i < 2 ? a + 4 * g + 2 * i : b + 4 * g + 2 * (i - 2);
+                        v[2 * i] = i8_scaled(r[0], sw[i], s.x);
+                        v[2 * i + 1] = i8_scaled(r[1], sw[i], s.y);
                     }
-                } else {
-                    // this warp's 16 tokens of the chunk: 0-15 (gate warp) or 16-31 (up warp)
-                    const int my_half = gate_warp ? 0 : 16;
-                    float *give = xb + xbuf * (2 * 16 * 32) + (gate_warp ? 0 : 16 * 32);
-                    const float *take = xb + xbuf * (2 * 16 * 32) + (gate_warp ? 16 * 32 : 0);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const int o = gate_warp ? 16 + j : j;            // the partner's tokens
-                        give[j * 32 + lane] = i8_scaled(gate_warp ? v[16 + j] : v[j], sw, sx[o]);
-                    }
-                    named_bar_sync(bar_xchg(pq), 64);
-                    if (f_ok) {
-                        uint16_t *dst = col + static_cast<size_t>(c0 + my_half) * p.m_out;
-                        const int n = ti.valid - c0 - my_half;
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            if (j < n) {
-                                const float other = take[j * 32 + lane];
-                                const float mine = i8_scaled(gate_warp ? v[j] : v[16 + j], sw, sx[my_half + j]);
-                                *dst = i8_act(gate_warp ? mine : other, gate_warp ? other : mine);
-                            }
-                            dst += p.m_out;
-                        }
+                    if constexpr (SWIGLU) {
+                        lo[g] = i8_bf16x2(i8_act(v[0], v[4]), i8_act(v[1], v[5]));
+                        hi[g] = i8_bf16x2(i8_act(v[2], v[6]), i8_act(v[3], v[7]));
+                        if (g & 1)
+                            stmatrix_x4_trans(st_addr + 8 * (g - 1) * C::kRowBytes, lo[g - 1], hi[g - 1], lo[g], hi[g]);
+                    } else {
+                        stmatrix_x4_trans(st_addr + 8 * g * C::kRowBytes, i8_bf16x2(v[0], v[1]), i8_bf16x2(v[2], v[3]),
+                                          i8_bf16x2(v[4], v[5]), i8_bf16x2(v[6], v[7]));
                     }
                 }
-                xbuf ^= 1;
+                __syncwarp();
+                const int piece = lane % kPieces;
+                if (f0 + 8 * piece < p.m_out) {
+#pragma unroll
+                    for (int i = 0; i < kPieces; ++i) {
+                        const int t = lane / kPieces + i * (32 / kPieces);
+                        const uint4 v = *reinterpret_cast<const uint4 *>(rows_s + t * C::kRowBytes + 16 * piece);
+                        if (32 * c + t < ti.valid)
+                            *reinterpret_cast<uint4 *>(p.out + static_cast<size_t>(ti.row0 + 32 * c + t) * p.m_out + f0 +
+                                                       8 * piece) = v;
+                    }
+                }
+                __syncwarp();
             };
             // two register sets: the next 32 columns load while this set is stored
-            const int c_end = 32 * c_hi;
-            uint32_t va[32], vb[32];
-            tmem_ld_32x32b_x32(tb + 32 * c_lo, va);
+            uint32_t a0[16], b0[16], a1[16], b1[16];
+            load(a0, b0, c_lo);
             tmem_wait_ld();
-            for (int c0 = 32 * c_lo;; c0 += 64) {
-                const bool more_a = c0 + 32 < c_end;
-                if (more_a) tmem_ld_32x32b_x32(tb + c0 + 32, vb); else release();
-                chunk(va, c0);
+            for (int c = c_lo;; c += 2) {
+                const bool more_a = c + 1 < c_hi;
+                if (more_a) load(a1, b1, c + 1); else release();
+                chunk(a0, b0, c);
                 if (!more_a) break;
                 tmem_wait_ld();
-                const bool more_b = c0 + 64 < c_end;
-                if (more_b) tmem_ld_32x32b_x32(tb + c0 + 64, va); else release();
-                chunk(vb, c0 + 32);
+                const bool more_b = c + 2 < c_hi;
+                if (more_b) load(a0, b0, c + 2); else release();
+                chunk(a1, b1, c + 1);
                 if (!more_b) break;
                 tmem_wait_ld();
             }
@@ -333,14 +320,15 @@ grouped_gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __gri
 
 template <bool SWIGLU>
 cudaError_t run_i8_pair(const I8GemmArgs &g, cudaStream_t s) {
-    constexpr int STAGES = SWIGLU ? 5 : 6;
+    constexpr int STAGES = 6;
     using C = I8PairCfg<SWIGLU, STAGES>;
     CUtensorMap ta, tb;
-    const uint64_t a_rows = static_cast<uint64_t>(g.base.E) * g.base.w_rows;
     const uint64_t K = static_cast<uint64_t>(g.base.K);
-    if (g.base.perm ||
-        !make_map(&ta, g.base.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, a_rows, kI8BK, SWIGLU ? 64 : 128,
-                  CU_TENSOR_MAP_SWIZZLE_128B) ||
+    const bool map_a = SWIGLU ? make_gate_up_map(&ta, g.base.w, g.base.E, g.base.m_out, K, 4)
+                              : make_map(&ta, g.base.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K,
+                                         static_cast<uint64_t>(g.base.E) * g.base.w_rows, kI8BK, 128,
+                                         CU_TENSOR_MAP_SWIZZLE_128B);
+    if (g.base.perm || !map_a ||
         !make_map(&tb, g.base.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, static_cast<uint64_t>(g.base.P), kI8BK, kBBox,
                   CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;

@@ -212,7 +212,8 @@ grouped_gemm_i8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
                     const float sx = __shfl_sync(0xffffffffu, sx_l, j);
                     if (f_ok && n < ti.valid) {
                         p.out[static_cast<size_t>(ti.row0 + n) * p.m_out + f] =
-                            SWIGLU ? i8_act(i8_scaled(g[j], sg, sx), i8_scaled(u[j], su, sx)) : i8_down(g[j], sg, sx);
+                            i8_bf16(SWIGLU ? i8_act(i8_scaled(g[j], sg, sx), i8_scaled(u[j], su, sx))
+                                           : i8_scaled(g[j], sg, sx));
                     }
                 }
             }
