@@ -102,6 +102,14 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volati
     return true;
 }
 
+// True in one lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}\n" : "=r"(r)::"memory");
+    return r != 0;
+}
+
 // ------------------------------------------------------ clusters (CTA pairs) --
 
 __device__ __forceinline__ uint32_t cluster_ctarank() {

@@ -56,12 +56,37 @@ struct I8PairCfg {
     static_assert(kSmemBytes + 64 <= kSmemLimit, "shared memory");
 };
 
-// decode_tile's row count rounded up to 32.
-__device__ __forceinline__ TileInfo pair_tile(int tile, const int *pre, const int *off, int E, int MB) {
-    TileInfo t = decode_tile(tile, pre, off, E, MB, kTokBlock);
-    t.n_mma = (t.valid + 31) & ~31;
-    return t;
-}
+// The tiles of this pair in order, for a converged warp: every 32 tiles each
+// lane decodes one of them (a search over the experts and two divisions, about
+// 800 cycles), and each tile is then a few shuffles.
+struct TileFeed {
+    const int *pre, *off;
+    int E, MB, tile, step, total, left;
+    TileInfo mine;
+
+    __device__ __forceinline__ TileFeed(const int *pre_, const int *off_, int E_, int MB_, int first, int step_)
+        : pre(pre_), off(off_), E(E_), MB(MB_), tile(first), step(step_), total(pre_[E_]), left(0) {}
+
+    // False when there is none left.
+    __device__ __forceinline__ bool next(TileInfo &t) {
+        if (tile >= total) return false;
+        if (left == 0) {
+            const int lane = threadIdx.x & 31;
+            const long long at = tile + static_cast<long long>(lane) * step;
+            mine = decode_tile(at < total ? static_cast<int>(at) : tile, pre, off, E, MB, kTokBlock);
+            left = 32;
+        }
+        const int src = 32 - left;
+        t.e = __shfl_sync(0xffffffffu, mine.e, src);
+        t.mb = __shfl_sync(0xffffffffu, mine.mb, src);
+        t.row0 = __shfl_sync(0xffffffffu, mine.row0, src);
+        t.valid = __shfl_sync(0xffffffffu, mine.valid, src);
+        t.n_mma = (t.valid + 31) & ~31;              // kind::i8 across a pair takes N in steps of 32
+        --left;
+        tile += step;
+        return true;
+    }
+};
 
 template <bool SWIGLU, int STAGES>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(320, 1)
@@ -121,71 +146,62 @@ grouped_gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __gri
     cluster_sync();                                          // barriers of both CTAs initialised
     tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_holder;
-    const int total_tiles = pre_s[E];
-    const int first_tile = static_cast<int>(cluster_id_x());
-    const int tile_step = static_cast<int>(cluster_count_x());
+    TileFeed feed(pre_s, off_s, E, MB, static_cast<int>(cluster_id_x()), static_cast<int>(cluster_count_x()));
+    TileInfo ti;
 
     if (warp == 0) {
         // ============================ TMA producer (both CTAs) ==================
-        if (lane == 0) {
-            const uint64_t pol = l2_policy_evict_last();
-            int stage = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            for (int tile = first_tile; tile < total_tiles && ok; tile += tile_step) {
-                const TileInfo ti = pair_tile(tile, pre_s, off_s, E, MB);
-                const int half = ti.n_mma / 2;                       // token rows from each CTA
-                const uint32_t tx = 2u * kStage;
-                const int b_row = ti.row0 + rank * half;             // the non-leading CTA's shift
-                for (int kb = 0; kb < KB; ++kb) {
-                    ok = mbar_wait(&empty_bar[stage], phase ^ 1, abort_flag, p.err, 128);
-                    if (!ok) break;
+        const uint64_t pol = l2_policy_evict_last();
+        const bool issuer = lane == 0;
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        while (ok && feed.next(ti)) {
+            const int b_row = ti.row0 + rank * (ti.n_mma / 2);       // the non-leading CTA's shift
+            const int a_row = ti.e * p.w_rows + ti.mb * 256 + 128 * rank;
+            for (int kb = 0; kb < KB; ++kb) {
+                ok = warp_wait(&empty_bar[stage], phase ^ 1, abort_flag, p.err, 64);
+                if (!ok) break;
+                if (issuer) {
                     const uint32_t full_leader = cluster_map(smem_u32(&full_bar[stage]), 0);
                     uint8_t *st = ring + stage * kStage;
-                    if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], tx);
+                    if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], 2u * kStage);
                     if (SWIGLU)
                         tma_load_5d_pair(st, &tmA, full_leader, kb * kI8BK, 0, 0, ti.mb * 8 + 4 * rank, ti.e, pol);
                     else
-                        tma_load_2d_pair(st, &tmA, full_leader, kb * kI8BK, ti.e * p.w_rows + ti.mb * 256 + 128 * rank,
-                                         pol);
+                        tma_load_2d_pair(st, &tmA, full_leader, kb * kI8BK, a_row, pol);
                     tma_load_2d_pair(st + kTileA, &tmB, full_leader, kb * kI8BK, b_row, pol);
-                    if (++stage == STAGES) { stage = 0; phase ^= 1; }
                 }
+                if (++stage == STAGES) { stage = 0; phase ^= 1; }
             }
         }
     } else if (warp == 1) {
         // ============================ MMA issuer (leading CTA) ==================
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
+            const uint32_t ring_lo = desc_low(smem_u32(ring));
             int stage = 0;
             uint32_t phase = 0;
             int buf = 0;
             uint32_t bphase = 0;
             bool ok = true;
-            for (int tile = first_tile; tile < total_tiles && ok; tile += tile_step) {
-                const TileInfo ti = pair_tile(tile, pre_s, off_s, E, MB);
+            while (ok && feed.next(ti)) {
                 const uint32_t idesc = idesc_i8_i32(kPairM, ti.n_mma);
-                ok = mbar_wait(&tempty_bar[buf], bphase ^ 1, abort_flag, p.err);
+                ok = warp_wait(&tempty_bar[buf], bphase ^ 1, abort_flag, p.err, 64);
                 if (!ok) break;
                 tc_fence_after_sync();
                 const uint32_t d = tmem_base + buf * kAccCols;
                 for (int kb = 0; kb < KB; ++kb) {
-                    ok = mbar_wait(&full_bar[stage], phase, abort_flag, p.err, 0);
+                    ok = warp_wait(&full_bar[stage], phase, abort_flag, p.err, 0);
                     if (!ok) break;
-                    tc_fence_after_sync();
-                    const uint32_t st = smem_u32(ring + stage * kStage);
-                    const uint64_t da = sw128_kmajor_desc(st);
-                    const uint64_t db = sw128_kmajor_desc(st + kTileA);
-#pragma unroll
-                    for (int k = 0; k < kI8BK / 32; ++k)
-                        umma_i8_ss_pair(d, da + 2 * k, db + 2 * k, idesc, (kb | k) != 0);
-                    umma_commit_pair(&empty_bar[stage], 0x3);
+                    const uint32_t a = ring_lo + stage * (kStage >> 4);
+                    umma_i8_stage_pair(d, a, a + (kTileA >> 4), idesc, kb != 0, &empty_bar[stage]);
                     if (++stage == STAGES) { stage = 0; phase ^= 1; }
                 }
                 if (!ok) break;
-                umma_commit_pair(&tfull_bar[buf], 0x3);
+                if (elect_one()) umma_commit_pair(&tfull_bar[buf], 0x3);
                 if (++buf == 2) { buf = 0; bphase ^= 1; }
             }
-            umma_commit_pair(drain_bar, 0x1);
+            if (elect_one()) umma_commit_pair(drain_bar, 0x1);
             volatile int never = 0;
             mbar_wait(drain_bar, 0, &never, p.err);
         }
@@ -214,8 +230,7 @@ grouped_gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __gri
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster_relaxed(buf ? tempty_leader1 : tempty_leader0);
         };
-        for (int tile = first_tile; tile < total_tiles; tile += tile_step) {
-            const TileInfo ti = pair_tile(tile, pre_s, off_s, E, MB);
+        while (feed.next(ti)) {
             // this half's columns: chunks [c_lo, c_hi) of 32 tokens
             const int nch = (ti.valid + 31) >> 5;
             const int split = (nch + 1) >> 1;
@@ -236,7 +251,7 @@ grouped_gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __gri
                 sx_s[n - 32 * c_lo] = n < ti.valid ? __ldg(ip.x_sf + ti.row0 + n) : 0.f;
             }
             __syncwarp();
-            if (!__shfl_sync(0xffffffffu, mbar_wait(&tfull_bar[buf], bphase, abort_flag, p.err, 512), 0)) break;
+            if (!warp_wait(&tfull_bar[buf], bphase, abort_flag, p.err, 128)) break;
             tc_fence_after_sync();
             if (c_lo >= c_hi) {
                 release();
