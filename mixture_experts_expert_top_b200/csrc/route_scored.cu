@@ -11,8 +11,14 @@
 //   ids = the top_k largest c of those groups, equal ones by the lower id
 //   w_j = scale * s_j / sum_i s_i (renormalised) or scale * s_j
 // Both scores rise with the logit, so without a bias the order is that of the
-// logits themselves, compared exactly. With one, two experts may differ in
-// the last bits of s + b alone: the order is decided in 64 bits.
+// logits themselves, compared exactly as fp32 keys. With one, two experts may
+// differ in the last bits of s + b alone, so the order is that of 64-bit
+// values: scores are formed in fp32 with a bound on their error, the selection
+// runs on them, and it stands if every gap that decided it (between
+// consecutive selected experts, to the first one left out, and between the
+// last group kept and the first one dropped) exceeds twice the bound. The few
+// rows where one does not (about 1 in 1000 for 256 experts) are selected again
+// from 64-bit scores (select_64).
 #include <math.h>
 
 #include "common.cuh"
@@ -153,6 +159,121 @@ __device__ __noinline__ int select_64(const RouterArgs &a, const float (&x)[N], 
     return my_id;
 }
 
+// fp32 scores of the lane's experts (lane l: l*N .. l*N+N-1) and a bound on
+// the error of c = s + b against its 64-bit value, the same in all lanes. In
+// units of u = 2^-24: expf is within 2 ulp (4u); a sigmoid adds two roundings;
+// a softmax term has its argument's rounding, u |l - m|, besides, the sum of E
+// terms at most N + 5 additions and its terms' average error (|l - m| averages
+// below ln E < 7 over a softmax), the quotient two. s |l - m| <= 0.37 s_max.
+// Adding b rounds by u |c|; infinities are exact.
+template <int N>
+__device__ __forceinline__ float scores_32(const RouterArgs &a, const float (&x)[N], float m, const float *bias, float (&s)[N],
+                                           float (&c)[N]) {
+    const int e0 = (threadIdx.x & 31) * N;
+    float top = 0.f, big = 0.f;
+    if (a.score == MOE_SCORE_SOFTMAX) {
+        float z = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            s[i] = x[i] == m ? (m == -INFINITY ? 0.f : 1.f) : expf(x[i] - m);
+            z += s[i];
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+        const float inv = z > 0.f ? 1.0f / z : 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[i] *= inv;
+        top = inv;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            s[i] = 1.0f / (1.0f + expf(-x[i]));
+            top = fmaxf(top, s[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        c[i] = bias && e0 + i < a.E ? s[i] + bias[e0 + i] : s[i];
+        if (fabsf(c[i]) < INFINITY) big = fmaxf(big, fabsf(c[i]));
+    }
+    // both maxima are of non-negative floats: their bits order them
+    big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
+    if (a.score == MOE_SCORE_SOFTMAX) return 0x1p-24f * 1.25f * ((N + 24.0f) * top + big) + 1e-37f;
+    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+    return 0x1p-24f * 1.25f * (6.0f * top + big) + 1e-37f;
+}
+
+// a > b by more than `gap`, for the values of two keys in descending order. A
+// missing candidate (key 0) is behind everything; equal keys are never apart.
+__device__ __forceinline__ bool apart(uint32_t ka, uint32_t kb, float gap) {
+    return kb == 0u || key_logit(ka) - key_logit(kb) > gap;
+}
+
+// The selection on fp32 values. by: what groups are valued by; c: what experts
+// are ordered by, exact when err is 0. Returns slot j's expert in lane j;
+// `sure` (the same in all lanes) says whether the 64-bit selection is the same.
+template <int N>
+__device__ __forceinline__ int select_32(const RouterArgs &a, const float (&by)[N], const float (&c)[N], float err_by,
+                                         float err_c, float *by_s, bool &sure) {
+    const int lane = threadIdx.x & 31;
+    const int e0 = lane * N;
+    sure = true;
+    uint32_t key[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) key[i] = e0 + i < a.E ? logit_key(c[i]) : 0u;
+    if (a.n_group > 1) {
+        const int size = a.E / a.n_group;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (e0 + i < a.E) by_s[e0 + i] = by[i] != by[i] ? -INFINITY : by[i];
+        __syncwarp();
+        float g = -INFINITY;
+        if (lane < a.n_group) {
+            float top1 = -INFINITY, top2 = -INFINITY;
+            for (int i = 0; i < size; ++i) {
+                const float v = by_s[lane * size + i];
+                top2 = fmaxf(top2, fminf(top1, v));
+                top1 = fmaxf(top1, v);
+            }
+            g = a.group_top == 2 ? top1 + top2 : top1;
+        }
+        const uint32_t gk = lane < a.n_group ? logit_key(g) : 0u;
+        const uint32_t kept = keep_groups(gk, a.n_group, a.topk_group);
+        if (err_by > 0.f && a.topk_group < a.n_group) {
+            // a sum of two: twice the error, and its own rounding below it
+            const uint32_t last = __reduce_min_sync(0xffffffffu, (kept >> lane) & 1u ? gk : 0xffffffffu);
+            const uint32_t first = __reduce_max_sync(0xffffffffu, (kept >> lane) & 1u ? 0u : gk);
+            sure = apart(last, first, (a.group_top == 2 ? 8.0f : 2.0f) * err_by);
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (e0 + i < a.E && !((kept >> ((e0 + i) / size)) & 1u)) key[i] = 0u;
+        __syncwarp();
+    }
+    int my_id = 0;
+    uint32_t before = 0;
+    const int rounds = err_c > 0.f ? a.k + 1 : a.k;              // one more to see the gap behind the last
+    for (int j = 0; j < rounds; ++j) {
+        uint32_t local = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) local = max(local, key[i]);
+        const uint32_t best = __reduce_max_sync(0xffffffffu, local);
+        if (err_c > 0.f && j > 0) sure = sure && apart(before, best, 2.0f * err_c);
+        before = best;
+        if (j == a.k) break;
+        uint32_t cand = 0xffffffffu;
+#pragma unroll
+        for (int i = N - 1; i >= 0; --i)
+            if (key[i] == best) cand = static_cast<uint32_t>(e0 + i);
+        const uint32_t bid = __reduce_min_sync(0xffffffffu, cand);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (static_cast<uint32_t>(e0 + i) == bid) key[i] = 0u;
+        if (lane == j) my_id = static_cast<int>(bid);
+    }
+    return my_id;
+}
+
 template <int N, typename L>
 __global__ void __launch_bounds__(kWarpsPerBlock * 32)
 route_scored_kernel(const RouterArgs a) {
@@ -177,7 +298,21 @@ route_scored_kernel(const RouterArgs a) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     }
-    const int id = select_64<N>(a, x, m, by_all + static_cast<size_t>(warp) * a.E);
+    double *by_s = by_all + static_cast<size_t>(warp) * a.E;
+    const bool by_logit = a.bias == nullptr;
+    int id;
+    bool sure;
+    if (by_logit && (a.n_group == 1 || a.group_top == 1)) {
+        id = select_32<N>(a, x, x, 0.f, 0.f, reinterpret_cast<float *>(by_s), sure);      // exact
+    } else {
+        float s[N], c[N];
+        const float err = scores_32<N>(a, x, m, a.bias, s, c);
+        if (by_logit)
+            id = select_32<N>(a, s, x, err, 0.f, reinterpret_cast<float *>(by_s), sure);
+        else
+            id = select_32<N>(a, c, c, err, err, reinterpret_cast<float *>(by_s), sure);
+        if (!sure) id = select_64<N>(a, x, m, by_s);
+    }
     // The weight of slot j, in lane j. Renormalised, only ratios of scores count:
     // softmax takes them relative to the largest selected logit, and so does a
     // sigmoid whose selected scores are all below e^-60 (there s = exp(l) to
