@@ -17,8 +17,7 @@
 // runs on them, and it stands if every gap that decided it (between
 // consecutive selected experts, to the first one left out, and between the
 // last group kept and the first one dropped) exceeds twice the bound. The few
-// rows where one does not (about 1 in 1000 for 256 experts) are selected again
-// from 64-bit scores (select_64).
+// rows where one does not are selected again from 64-bit scores (select_64).
 #include <math.h>
 
 #include "common.cuh"
@@ -39,10 +38,44 @@ struct RouterArgs {
     float scale;
     int32_t *ids;
     float *w;
+    int vec;                                // rows and lanes' shares are 16-byte aligned
+    int group_lanes;                        // lanes that hold one group, a power of two; 0: groups end inside lanes
 };
 
 __device__ __forceinline__ float load_logit(const float *p) { return *p; }
 __device__ __forceinline__ float load_logit(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
+
+// The lane's N consecutive values from e0 on (`fill` past E), in 16-byte loads where `vec` allows.
+template <int N>
+__device__ __forceinline__ void load_lane(const float *row, int e0, int E, bool vec, float fill, float (&x)[N]) {
+    if (N % 4 == 0 && vec) {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            const float4 v = e0 < E ? *reinterpret_cast<const float4 *>(row + e0 + 4 * i) : make_float4(fill, fill, fill, fill);
+            x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = e0 + i < E ? row[e0 + i] : fill;
+}
+
+template <int N>
+__device__ __forceinline__ void load_lane(const __nv_bfloat16 *row, int e0, int E, bool vec, float fill, float (&x)[N]) {
+    if (N % 8 == 0 && vec) {
+#pragma unroll
+        for (int i = 0; i < N / 8; ++i) {
+            const uint4 v = e0 < E ? *reinterpret_cast<const uint4 *>(row + e0 + 8 * i) : make_uint4(0, 0, 0, 0);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                x[8 * i + j] = e0 < E ? bf16_bits_to_float((w[j >> 1] >> (16 * (j & 1))) & 0xFFFFu) : fill;
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = e0 + i < E ? __bfloat162float(row[e0 + i]) : fill;
+}
 
 // The logit as the scores take it: NaN is -inf, -0 is +0.
 __device__ __forceinline__ float clean_logit(float x) {
@@ -159,23 +192,25 @@ __device__ __noinline__ int select_64(const RouterArgs &a, const float (&x)[N], 
     return my_id;
 }
 
-// fp32 scores of the lane's experts (lane l: l*N .. l*N+N-1) and a bound on
-// the error of c = s + b against its 64-bit value, the same in all lanes. In
-// units of u = 2^-24: expf is within 2 ulp (4u); a sigmoid adds two roundings;
-// a softmax term has its argument's rounding, u |l - m|, besides, the sum of E
-// terms at most N + 5 additions and its terms' average error (|l - m| averages
-// below ln E < 7 over a softmax), the quotient two. s |l - m| <= 0.37 s_max.
-// Adding b rounds by u |c|; infinities are exact.
+// fp32 scores s and choices c = s + b of the lane's experts (lane l: l*N ..
+// l*N+N-1), and a bound on |c - its 64-bit value|, the same in all lanes. In
+// units of u = 2^-24: __expf is within 2 + 1.173 |x| ulp, (4 + 2.35 |x|) u;
+// __fdividef within 2 ulp, 4u; adding b rounds by u |c|. A sigmoid passes on
+// (1 - s) of its exponential's error: min(s (4 + 2.35 |x|), 1.6) u, since s (1 -
+// s) <= 0.25 and s (1 - s) |x| <= 0.23. A softmax term has its argument's
+// rounding, u |d|, d = l - m, besides; s |d| <= 0.37 s_max; the sum of the terms
+// adds N + 5 roundings and its terms' average error (|d| averages below ln E <
+// 7 over a softmax). The factor 1.25 covers the products of errors.
 template <int N>
-__device__ __forceinline__ float scores_32(const RouterArgs &a, const float (&x)[N], float m, const float *bias, float (&s)[N],
-                                           float (&c)[N]) {
+__device__ __forceinline__ float scores_32(const RouterArgs &a, const float (&x)[N], float m, float (&s)[N], float (&c)[N]) {
     const int e0 = (threadIdx.x & 31) * N;
-    float top = 0.f, big = 0.f;
-    if (a.score == MOE_SCORE_SOFTMAX) {
+    float err = 0.f, big = 0.f;
+    const bool soft = a.score == MOE_SCORE_SOFTMAX;
+    if (soft) {
         float z = 0.f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            s[i] = x[i] == m ? (m == -INFINITY ? 0.f : 1.f) : expf(x[i] - m);
+            s[i] = x[i] == m ? (m == -INFINITY ? 0.f : 1.f) : __expf(x[i] - m);
             z += s[i];
         }
 #pragma unroll
@@ -183,24 +218,31 @@ __device__ __forceinline__ float scores_32(const RouterArgs &a, const float (&x)
         const float inv = z > 0.f ? 1.0f / z : 0.f;
 #pragma unroll
         for (int i = 0; i < N; ++i) s[i] *= inv;
-        top = inv;
+        err = (N + 45.0f) * inv;
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            s[i] = 1.0f / (1.0f + expf(-x[i]));
-            top = fmaxf(top, s[i]);
+            s[i] = __fdividef(1.0f, 1.0f + __expf(-x[i]));
+            if (x[i] > -INFINITY) err = fmaxf(err, s[i] * fmaf(2.35f, fabsf(x[i]), 4.0f));
+            big = fmaxf(big, s[i]);
         }
+        err = fminf(err, 1.6f) + 6.0f * big;
     }
+    if (a.bias) {
+        float b[N];
+        load_lane<N>(a.bias, e0, a.E, a.vec, 0.f, b);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        c[i] = bias && e0 + i < a.E ? s[i] + bias[e0 + i] : s[i];
-        if (fabsf(c[i]) < INFINITY) big = fmaxf(big, fabsf(c[i]));
+        for (int i = 0; i < N; ++i) {
+            c[i] = fmaxf(s[i] + b[i], -INFINITY);                // NaN counts as -inf
+            if (fabsf(c[i]) < INFINITY) big = fmaxf(big, fabsf(c[i]));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) c[i] = s[i];
     }
-    // both maxima are of non-negative floats: their bits order them
-    big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
-    if (a.score == MOE_SCORE_SOFTMAX) return 0x1p-24f * 1.25f * ((N + 24.0f) * top + big) + 1e-37f;
-    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-    return 0x1p-24f * 1.25f * (6.0f * top + big) + 1e-37f;
+    // a maximum over lanes of non-negative floats: their bits order them
+    err = 0x1p-24f * 1.25f * (err + big) + 1e-37f;
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(err)));
 }
 
 // a > b by more than `gap`, for the values of two keys in descending order. A
@@ -209,58 +251,72 @@ __device__ __forceinline__ bool apart(uint32_t ka, uint32_t kb, float gap) {
     return kb == 0u || key_logit(ka) - key_logit(kb) > gap;
 }
 
-// The selection on fp32 values. by: what groups are valued by; c: what experts
-// are ordered by, exact when err is 0. Returns slot j's expert in lane j;
-// `sure` (the same in all lanes) says whether the 64-bit selection is the same.
+// Whether each of the lane's experts is in a kept group, as bits. by: what
+// groups are valued by, within err_by of its 64-bit value.
 template <int N>
-__device__ __forceinline__ int select_32(const RouterArgs &a, const float (&by)[N], const float (&c)[N], float err_by,
-                                         float err_c, float *by_s, bool &sure) {
+__device__ __forceinline__ uint32_t kept_experts(const RouterArgs &a, const float (&by)[N], float err_by, float *by_s, bool &sure) {
     const int lane = threadIdx.x & 31;
     const int e0 = lane * N;
-    sure = true;
-    uint32_t key[N];
+    const int size = a.E / a.n_group;
+    float top1 = -INFINITY, top2 = -INFINITY;
+    auto add = [&](float v) {
+        top2 = fmaxf(top2, fminf(top1, v));
+        top1 = fmaxf(top1, v);
+    };
+    uint32_t gk = 0, kept, bits = 0;
+    const int gl = a.group_lanes;
+    if (gl) {
+        // whole lanes per group: each group's two largest by exchanges inside its lanes
 #pragma unroll
-    for (int i = 0; i < N; ++i) key[i] = e0 + i < a.E ? logit_key(c[i]) : 0u;
-    if (a.n_group > 1) {
-        const int size = a.E / a.n_group;
+        for (int i = 0; i < N; ++i) add(e0 + i < a.E ? by[i] : -INFINITY);
+        for (int o = 1; o < gl; o <<= 1) {
+            const float u1 = __shfl_xor_sync(0xffffffffu, top1, o), u2 = __shfl_xor_sync(0xffffffffu, top2, o);
+            top2 = fmaxf(fminf(top1, u1), fmaxf(top2, u2));
+            top1 = fmaxf(top1, u1);
+        }
+        // group g's value moves to lane g
+        const float mine = a.group_top == 2 ? top1 + top2 : top1;
+        const float g = __shfl_sync(0xffffffffu, mine, (lane * gl) & 31);
+        gk = lane < a.n_group ? logit_key(g) : 0u;
+    } else {
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            if (e0 + i < a.E) by_s[e0 + i] = by[i] != by[i] ? -INFINITY : by[i];
+            if (e0 + i < a.E) by_s[e0 + i] = by[i];
         __syncwarp();
-        float g = -INFINITY;
         if (lane < a.n_group) {
-            float top1 = -INFINITY, top2 = -INFINITY;
-            for (int i = 0; i < size; ++i) {
-                const float v = by_s[lane * size + i];
-                top2 = fmaxf(top2, fminf(top1, v));
-                top1 = fmaxf(top1, v);
-            }
-            g = a.group_top == 2 ? top1 + top2 : top1;
+            for (int i = 0; i < size; ++i) add(by_s[lane * size + i]);
+            gk = logit_key(a.group_top == 2 ? top1 + top2 : top1);
         }
-        const uint32_t gk = lane < a.n_group ? logit_key(g) : 0u;
-        const uint32_t kept = keep_groups(gk, a.n_group, a.topk_group);
-        if (err_by > 0.f && a.topk_group < a.n_group) {
-            // a sum of two: twice the error, and its own rounding below it
-            const uint32_t last = __reduce_min_sync(0xffffffffu, (kept >> lane) & 1u ? gk : 0xffffffffu);
-            const uint32_t first = __reduce_max_sync(0xffffffffu, (kept >> lane) & 1u ? 0u : gk);
-            sure = apart(last, first, (a.group_top == 2 ? 8.0f : 2.0f) * err_by);
-        }
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (e0 + i < a.E && !((kept >> ((e0 + i) / size)) & 1u)) key[i] = 0u;
         __syncwarp();
     }
+    kept = keep_groups(gk, a.n_group, a.topk_group);
+    if (err_by > 0.f && a.topk_group < a.n_group) {
+        // a sum of two: twice the error, and its own rounding below it
+        const uint32_t last = __reduce_min_sync(0xffffffffu, (kept >> lane) & 1u ? gk : 0xffffffffu);
+        const uint32_t first = __reduce_max_sync(0xffffffffu, (kept >> lane) & 1u ? 0u : gk);
+        sure = apart(last, first, (a.group_top == 2 ? 8.0f : 2.0f) * err_by);
+    }
+    if (gl) return (kept >> (lane / gl)) & 1u ? 0xffffffffu : 0u;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (e0 + i < a.E) bits |= ((kept >> ((e0 + i) / size)) & 1u) << i;
+    return bits;
+}
+
+// The selection by the logits themselves, exact. Returns slot j's expert in lane j.
+template <int N>
+__device__ __forceinline__ int select_logits(const RouterArgs &a, const float (&x)[N], uint32_t bits) {
+    const int lane = threadIdx.x & 31;
+    const int e0 = lane * N;
+    uint32_t key[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) key[i] = e0 + i < a.E && ((bits >> i) & 1u) ? logit_key(x[i]) : 0u;
     int my_id = 0;
-    uint32_t before = 0;
-    const int rounds = err_c > 0.f ? a.k + 1 : a.k;              // one more to see the gap behind the last
-    for (int j = 0; j < rounds; ++j) {
+    for (int j = 0; j < a.k; ++j) {
         uint32_t local = 0;
 #pragma unroll
         for (int i = 0; i < N; ++i) local = max(local, key[i]);
         const uint32_t best = __reduce_max_sync(0xffffffffu, local);
-        if (err_c > 0.f && j > 0) sure = sure && apart(before, best, 2.0f * err_c);
-        before = best;
-        if (j == a.k) break;
         uint32_t cand = 0xffffffffu;
 #pragma unroll
         for (int i = N - 1; i >= 0; --i)
@@ -270,6 +326,64 @@ __device__ __forceinline__ int select_32(const RouterArgs &a, const float (&by)[
         for (int i = 0; i < N; ++i)
             if (static_cast<uint32_t>(e0 + i) == bid) key[i] = 0u;
         if (lane == j) my_id = static_cast<int>(bid);
+    }
+    return my_id;
+}
+
+// The selection by c, within err of its 64-bit value. A key holds c on a grid
+// between the smallest and the largest finite choice above the inverted expert
+// id (10 bits; 8 for N <= 8), so keys differ and one reduction finds a winner.
+// `sure` stays true if every gap is beyond the errors and the grid.
+template <int N>
+__device__ __forceinline__ int select_choices(const RouterArgs &a, const float (&c)[N], float err, uint32_t bits, bool &sure) {
+    constexpr int kIdBits = N <= 8 ? 8 : 10;
+    constexpr uint32_t kIdMask = (1u << kIdBits) - 1u;
+    constexpr float kSteps = static_cast<float>((1u << (32 - kIdBits)) - 4u);
+    const int lane = threadIdx.x & 31;
+    const int e0 = lane * N;
+    // the range: order-preserving keys of the finite choices
+    uint32_t least = 0xffffffffu, most = 0u;
+    bool inf = false;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const bool in = e0 + i < a.E && ((bits >> i) & 1u);
+        const uint32_t b = __float_as_uint(c[i]);
+        const uint32_t o = b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+        if (in && c[i] > -INFINITY) {
+            least = min(least, o);
+            most = max(most, o);
+        }
+        inf = inf || (in && c[i] == INFINITY);
+    }
+    least = __reduce_min_sync(0xffffffffu, least);
+    most = __reduce_max_sync(0xffffffffu, most);
+    const float lo = key_logit(least), hi = key_logit(most);
+    const float unit = kSteps / (hi - lo);
+    const float gap = ceilf(2.0f * err * unit) + 8.0f;           // 2 err, and each key's 3 roundings
+    // no finite choice, one value, an infinity, or a range that the grid does not resolve
+    sure = sure && !__any_sync(0xffffffffu, inf) && least < most && unit < 3e37f && gap < kSteps;
+    const uint32_t gap_key = sure ? static_cast<uint32_t>(gap) : 0u;
+    uint32_t key[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const bool in = e0 + i < a.E && ((bits >> i) & 1u);
+        const uint32_t grid = c[i] > -INFINITY ? 1u + __float2uint_rn((c[i] - lo) * unit) : 0u;
+        key[i] = in ? (grid << kIdBits) | (kIdMask - static_cast<uint32_t>(e0 + i)) : 0u;
+    }
+    int my_id = 0;
+    uint32_t before = 0;
+    for (int j = 0; j <= a.k; ++j) {                             // one more than k to see the gap behind the last
+        uint32_t local = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) local = max(local, key[i]);
+        const uint32_t best = __reduce_max_sync(0xffffffffu, local);
+        if (j > 0) sure = sure && (best == 0u || (before >> kIdBits) - (best >> kIdBits) > gap_key);
+        before = best;
+        if (j == a.k) break;
+        sure = sure && (best >> kIdBits) != 0u;                  // an expert that is switched off: exact ties
+#pragma unroll
+        for (int i = 0; i < N; ++i) key[i] = key[i] == best ? 0u : key[i];
+        if (lane == j) my_id = static_cast<int>(kIdMask - (best & kIdMask));
     }
     return my_id;
 }
@@ -289,9 +403,10 @@ route_scored_kernel(const RouterArgs a) {
     const bool soft = a.score == MOE_SCORE_SOFTMAX;
     float x[N];
     float m = -INFINITY;
+    load_lane<N>(row, e0, a.E, a.vec, -INFINITY, x);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        x[i] = e0 + i < a.E ? clean_logit(load_logit(row + e0 + i)) : -INFINITY;
+        x[i] = clean_logit(x[i]);
         m = fmaxf(m, x[i]);
     }
     if (soft) {
@@ -301,16 +416,21 @@ route_scored_kernel(const RouterArgs a) {
     double *by_s = by_all + static_cast<size_t>(warp) * a.E;
     const bool by_logit = a.bias == nullptr;
     int id;
-    bool sure;
-    if (by_logit && (a.n_group == 1 || a.group_top == 1)) {
-        id = select_32<N>(a, x, x, 0.f, 0.f, reinterpret_cast<float *>(by_s), sure);      // exact
+    uint32_t bits = 0xffffffffu;
+    bool sure = true;
+    if (by_logit && a.n_group == 1) {
+        id = select_logits<N>(a, x, bits);
     } else {
         float s[N], c[N];
-        const float err = scores_32<N>(a, x, m, a.bias, s, c);
-        if (by_logit)
-            id = select_32<N>(a, s, x, err, 0.f, reinterpret_cast<float *>(by_s), sure);
-        else
-            id = select_32<N>(a, c, c, err, err, reinterpret_cast<float *>(by_s), sure);
+        float err = 0.f;
+        if (!by_logit || a.group_top == 2) err = scores_32<N>(a, x, m, s, c);
+        if (a.n_group > 1) {
+            if (err > 0.f)
+                bits = kept_experts<N>(a, c, err, reinterpret_cast<float *>(by_s), sure);
+            else
+                bits = kept_experts<N>(a, x, 0.f, reinterpret_cast<float *>(by_s), sure);    // exact
+        }
+        id = by_logit ? select_logits<N>(a, x, bits) : select_choices<N>(a, c, err, bits, sure);
         if (!sure) id = select_64<N>(a, x, m, by_s);
     }
     // The weight of slot j, in lane j. Renormalised, only ratios of scores count:
@@ -358,7 +478,11 @@ route_scored_kernel(const RouterArgs a) {
 }
 
 template <int N, typename L>
-cudaError_t launch_n(const RouterArgs &a, cudaStream_t s) {
+cudaError_t launch_n(RouterArgs a, cudaStream_t s) {
+    a.vec = a.E % N == 0 && N * sizeof(L) % 16 == 0 && N % 4 == 0 && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 &&
+            reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
+    const int size = a.E / a.n_group, lanes = size / N;
+    a.group_lanes = size % N == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
     const int blocks = (a.T + kWarpsPerBlock - 1) / kWarpsPerBlock;
     const size_t sm = a.n_group > 1 ? static_cast<size_t>(kWarpsPerBlock) * a.E * sizeof(double) : 0;
     return launch_pdl(route_scored_kernel<N, L>, dim3(blocks), dim3(kWarpsPerBlock * 32), sm, s, a);
