@@ -77,10 +77,19 @@ __device__ __forceinline__ void load_lane(const __nv_bfloat16 *row, int e0, int 
     for (int i = 0; i < N; ++i) x[i] = e0 + i < E ? __bfloat162float(row[e0 + i]) : fill;
 }
 
-// The logit as the scores take it: NaN is -inf, -0 is +0.
-__device__ __forceinline__ float clean_logit(float x) {
-    if (x != x) return -INFINITY;
-    return x == 0.f ? 0.f : x;
+// The logit as the scores take it: NaN is -inf (logit_key makes -0 equal +0).
+__device__ __forceinline__ float clean_logit(float x) { return fmaxf(x, -INFINITY); }
+
+__device__ __forceinline__ float warp_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+__device__ __forceinline__ float warp_min(float v) {
+    float r;
+    asm volatile("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
 }
 
 // Order-preserving map of a double onto uint64 (larger value, larger key); NaN
@@ -114,12 +123,16 @@ __device__ __forceinline__ uint32_t keep_groups(Key mine, int n_group, int keep)
     return __ballot_sync(0xffffffffu, lane < n_group && ahead < keep);
 }
 
-// The selection in 64 bits. Lane l holds experts l*N .. l*N+N-1 (x: their
-// cleaned logits, below E). Returns slot j's expert in lane j.
-template <int N>
-__device__ __noinline__ int select_64(const RouterArgs &a, const float (&x)[N], float m, double *by_s) {
+// The selection in 64 bits. Lane l holds experts l*N .. l*N+N-1. Returns slot
+// j's expert in lane j. It reads its logits again, so that the callers that
+// rarely need it keep theirs in registers.
+template <int N, typename L>
+__device__ __noinline__ int select_64(const RouterArgs &a, const L *row, float m, double *by_s) {
     const int lane = threadIdx.x & 31;
     const int e0 = lane * N;
+    float x[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = e0 + i < a.E ? clean_logit(load_logit(row + e0 + i)) : -INFINITY;
     const bool soft = a.score == MOE_SCORE_SOFTMAX;
     const bool by_logit = a.bias == nullptr;                     // experts are ordered by their logits
     const bool groups_by_logit = by_logit && a.group_top == 1;
@@ -192,21 +205,30 @@ __device__ __noinline__ int select_64(const RouterArgs &a, const float (&x)[N], 
     return my_id;
 }
 
+// Reciprocal within 1 ulp (2^-23 relative), 0 for +inf.
+__device__ __forceinline__ float fast_rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // fp32 scores s and choices c = s + b of the lane's experts (lane l: l*N ..
-// l*N+N-1), and a bound on |c - its 64-bit value|, the same in all lanes. In
-// units of u = 2^-24: __expf is within 2 + 1.173 |x| ulp, (4 + 2.35 |x|) u;
-// __fdividef within 2 ulp, 4u; adding b rounds by u |c|. A sigmoid passes on
-// (1 - s) of its exponential's error: min(s (4 + 2.35 |x|), 1.6) u, since s (1 -
-// s) <= 0.25 and s (1 - s) |x| <= 0.23. A softmax term has its argument's
-// rounding, u |d|, d = l - m, besides; s |d| <= 0.37 s_max; the sum of the terms
-// adds N + 5 roundings and its terms' average error (|d| averages below ln E <
-// 7 over a softmax). The factor 1.25 covers the products of errors.
+// l*N+N-1), their smallest and largest value over the row, and a bound on |c -
+// its 64-bit value|. In units of u = 2^-24: __expf is within 2 + 1.173 |x| ulp,
+// (4 + 2.35 |x|) u; the reciprocal within 2u; adding b rounds by u |c|. A
+// sigmoid passes on (1 - s) of its exponential's error: below 1.6 u, since s (1
+// - s) <= 0.25 and s (1 - s) |x| <= 0.23; its sum 1 + e adds one and its
+// reciprocal two of s <= 1: 4.6. A softmax term has its argument's rounding,
+// u |d|, d = l - m, besides; s |d| <= 0.37 s_max; the sum of the terms adds N + 5
+// roundings and its terms' average error (|d| averages below ln E < 7 over a
+// softmax). The factor 1.25 covers the products of errors, 1e-37 what the
+// exponential or the reciprocal flushes to zero.
 template <int N>
-__device__ __forceinline__ float scores_32(const RouterArgs &a, const float (&x)[N], float m, float (&s)[N], float (&c)[N]) {
+__device__ __forceinline__ float scores_32(const RouterArgs &a, const float (&x)[N], float m, float (&s)[N], float (&c)[N],
+                                           float &lo, float &hi) {
     const int e0 = (threadIdx.x & 31) * N;
-    float err = 0.f, big = 0.f;
-    const bool soft = a.score == MOE_SCORE_SOFTMAX;
-    if (soft) {
+    float err;
+    if (a.score == MOE_SCORE_SOFTMAX) {
         float z = 0.f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -221,34 +243,57 @@ __device__ __forceinline__ float scores_32(const RouterArgs &a, const float (&x)
         err = (N + 45.0f) * inv;
     } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            s[i] = __fdividef(1.0f, 1.0f + __expf(-x[i]));
-            if (x[i] > -INFINITY) err = fmaxf(err, s[i] * fmaf(2.35f, fabsf(x[i]), 4.0f));
-            big = fmaxf(big, s[i]);
-        }
-        err = fminf(err, 1.6f) + 6.0f * big;
+        for (int i = 0; i < N; ++i) s[i] = fast_rcp(1.0f + __expf(-x[i]));
+        err = 4.6f;
     }
-    if (a.bias) {
-        float b[N];
-        load_lane<N>(a.bias, e0, a.E, a.vec, 0.f, b);
+    float b[N];
+    if (a.bias) load_lane<N>(a.bias, e0, a.E, a.vec, 0.f, b);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            c[i] = fmaxf(s[i] + b[i], -INFINITY);                // NaN counts as -inf
-            if (fabsf(c[i]) < INFINITY) big = fmaxf(big, fabsf(c[i]));
-        }
-    } else {
+    for (int i = 0; i < N; ++i) c[i] = a.bias ? fmaxf(s[i] + b[i], -INFINITY) : s[i];    // NaN counts as -inf
+    lo = INFINITY;
+    hi = -INFINITY;
+    // with `vec` a lane's experts are all below E or none is
+    if (!a.vec || e0 < a.E) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) c[i] = s[i];
+        for (int i = 0; i < N; ++i)
+            if (a.vec || e0 + i < a.E) {
+                lo = fminf(lo, c[i]);
+                hi = fmaxf(hi, c[i]);
+            }
     }
-    // a maximum over lanes of non-negative floats: their bits order them
-    err = 0x1p-24f * 1.25f * (err + big) + 1e-37f;
-    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(err)));
+    lo = warp_min(lo);
+    hi = warp_max(hi);
+    if (lo == -INFINITY) {                                           // experts that are switched off
+        lo = INFINITY;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (e0 + i < a.E && c[i] > -INFINITY) lo = fminf(lo, c[i]);
+        lo = warp_min(lo);
+    }
+    return 0x1p-24f * 1.25f * (err + fmaxf(fabsf(lo), fabsf(hi))) + 1e-37f;
 }
 
 // a > b by more than `gap`, for the values of two keys in descending order. A
 // missing candidate (key 0) is behind everything; equal keys are never apart.
 __device__ __forceinline__ bool apart(uint32_t ka, uint32_t kb, float gap) {
     return kb == 0u || key_logit(ka) - key_logit(kb) > gap;
+}
+
+// Lane g holds group g's value as a key (0 from n_group on): the mask of the
+// topk_group largest, equal ones by the lower index; the last one kept and the
+// first one dropped (0: none).
+__device__ __forceinline__ uint32_t pick_groups(const RouterArgs &a, uint32_t gk, uint32_t &last, uint32_t &first) {
+    const int lane = threadIdx.x & 31;
+    uint32_t kept = 0;
+    last = 0;
+    for (int j = 0; j < a.topk_group; ++j) {
+        last = __reduce_max_sync(0xffffffffu, gk);
+        const int win = __ffs(__ballot_sync(0xffffffffu, gk == last && lane < a.n_group && !((kept >> lane) & 1u))) - 1;
+        kept |= 1u << win;
+        if (lane == win) gk = 0u;
+    }
+    first = __reduce_max_sync(0xffffffffu, gk);
+    return kept;
 }
 
 // Whether each of the lane's experts is in a kept group, as bits. by: what
@@ -263,7 +308,7 @@ __device__ __forceinline__ uint32_t kept_experts(const RouterArgs &a, const floa
         top2 = fmaxf(top2, fminf(top1, v));
         top1 = fmaxf(top1, v);
     };
-    uint32_t gk = 0, kept, bits = 0;
+    uint32_t gk = 0;
     const int gl = a.group_lanes;
     if (gl) {
         // whole lanes per group: each group's two largest by exchanges inside its lanes
@@ -289,13 +334,10 @@ __device__ __forceinline__ uint32_t kept_experts(const RouterArgs &a, const floa
         }
         __syncwarp();
     }
-    kept = keep_groups(gk, a.n_group, a.topk_group);
-    if (err_by > 0.f && a.topk_group < a.n_group) {
-        // a sum of two: twice the error, and its own rounding below it
-        const uint32_t last = __reduce_min_sync(0xffffffffu, (kept >> lane) & 1u ? gk : 0xffffffffu);
-        const uint32_t first = __reduce_max_sync(0xffffffffu, (kept >> lane) & 1u ? 0u : gk);
-        sure = apart(last, first, (a.group_top == 2 ? 8.0f : 2.0f) * err_by);
-    }
+    uint32_t last, first, bits = 0;
+    const uint32_t kept = pick_groups(a, gk, last, first);
+    // a sum of two: twice the error, and its own rounding below it
+    if (err_by > 0.f) sure = apart(last, first, (a.group_top == 2 ? 8.0f : 2.0f) * err_by);
     if (gl) return (kept >> (lane / gl)) & 1u ? 0xffffffffu : 0u;
 #pragma unroll
     for (int i = 0; i < N; ++i)
@@ -330,67 +372,107 @@ __device__ __forceinline__ int select_logits(const RouterArgs &a, const float (&
     return my_id;
 }
 
-// The selection by c, within err of its 64-bit value. A key holds c on a grid
-// between the smallest and the largest finite choice above the inverted expert
-// id (10 bits; 8 for N <= 8), so keys differ and one reduction finds a winner.
-// `sure` stays true if every gap is beyond the errors and the grid.
+// Keys in descending order (odd-even merge sort, every step unrolled).
 template <int N>
-__device__ __forceinline__ int select_choices(const RouterArgs &a, const float (&c)[N], float err, uint32_t bits, bool &sure) {
-    constexpr int kIdBits = N <= 8 ? 8 : 10;
+__device__ __forceinline__ void sort_keys(uint32_t (&key)[N]) {
+#pragma unroll
+    for (int p = 1; p < N; p *= 2)
+#pragma unroll
+        for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+            for (int j = q % p; j + q < N; j += 2 * q)
+#pragma unroll
+                for (int i = 0; i < q && i + j + q < N; ++i)
+                    if ((i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+                        const uint32_t hi = max(key[i + j], key[i + j + q]), lo = min(key[i + j], key[i + j + q]);
+                        key[i + j] = hi;
+                        key[i + j + q] = lo;
+                    }
+}
+
+// The selection by c, within err of its 64-bit value. A key holds c on a grid
+// from the smallest finite choice lo to the largest, hi, above the inverted
+// expert id, so keys differ: each lane sorts its own once (minima and maxima
+// only), and a slot takes one reduction over the lanes' largest. Grid value 0
+// is an expert that is switched off. `sure` stays true if every gap is beyond
+// the errors and the grid. Returns slot j's expert in lane j.
+template <int N>
+__device__ __forceinline__ int select_choices(const RouterArgs &a, const float (&c)[N], float err, float lo, float hi,
+                                              float *by_s, bool &sure) {
+    constexpr int kIdBits = N <= 16 ? 9 : 10;
     constexpr uint32_t kIdMask = (1u << kIdBits) - 1u;
     constexpr float kSteps = static_cast<float>((1u << (32 - kIdBits)) - 4u);
+    constexpr float kMagic = 8388608.0f + 1.0f;                  // 2^23: a grid value lands in the low mantissa bits
     const int lane = threadIdx.x & 31;
     const int e0 = lane * N;
-    // the range: order-preserving keys of the finite choices
-    uint32_t least = 0xffffffffu, most = 0u;
-    bool inf = false;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const bool in = e0 + i < a.E && ((bits >> i) & 1u);
-        const uint32_t b = __float_as_uint(c[i]);
-        const uint32_t o = b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
-        if (in && c[i] > -INFINITY) {
-            least = min(least, o);
-            most = max(most, o);
-        }
-        inf = inf || (in && c[i] == INFINITY);
-    }
-    least = __reduce_min_sync(0xffffffffu, least);
-    most = __reduce_max_sync(0xffffffffu, most);
-    const float lo = key_logit(least), hi = key_logit(most);
+    const int gl = a.n_group > 1 ? a.group_lanes : 0;
+    uint32_t bits = 0xffffffffu;
+    if (a.n_group > 1 && !gl) bits = kept_experts<N>(a, c, err, by_s, sure);
     const float unit = kSteps / (hi - lo);
     const float gap = ceilf(2.0f * err * unit) + 8.0f;           // 2 err, and each key's 3 roundings
-    // no finite choice, one value, an infinity, or a range that the grid does not resolve
-    sure = sure && !__any_sync(0xffffffffu, inf) && least < most && unit < 3e37f && gap < kSteps;
-    const uint32_t gap_key = sure ? static_cast<uint32_t>(gap) : 0u;
+    // one value, an infinity, or a range that the grid does not resolve: not here
+    sure = sure && lo < hi && hi < INFINITY && unit < 3e37f && gap < kSteps;
+    if (!sure) return 0;
+    const uint32_t gap_key = static_cast<uint32_t>(gap);
     uint32_t key[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const bool in = e0 + i < a.E && ((bits >> i) & 1u);
-        const uint32_t grid = c[i] > -INFINITY ? 1u + __float2uint_rn((c[i] - lo) * unit) : 0u;
-        key[i] = in ? (grid << kIdBits) | (kIdMask - static_cast<uint32_t>(e0 + i)) : 0u;
-    }
-    int my_id = 0;
-    uint32_t before = 0;
-    for (int j = 0; j <= a.k; ++j) {                             // one more than k to see the gap behind the last
-        uint32_t local = 0;
+    for (int i = 0; i < N; ++i)                                  // -inf gives a zero mantissa: grid value 0
+        key[i] = __float_as_uint(fmaf(c[i] - lo, unit, kMagic)) * (1u << kIdBits) + (kIdMask - static_cast<uint32_t>(e0 + i));
+    if (a.vec) {
+        if (e0 >= a.E)
 #pragma unroll
-        for (int i = 0; i < N; ++i) local = max(local, key[i]);
-        const uint32_t best = __reduce_max_sync(0xffffffffu, local);
-        if (j > 0) sure = sure && (best == 0u || (before >> kIdBits) - (best >> kIdBits) > gap_key);
+            for (int i = 0; i < N; ++i) key[i] = 0u;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) key[i] = e0 + i < a.E && ((bits >> i) & 1u) ? key[i] : 0u;
+    }
+    if (a.vec && bits != 0xffffffffu)
+#pragma unroll
+        for (int i = 0; i < N; ++i) key[i] = (bits >> i) & 1u ? key[i] : 0u;
+    sort_keys<N>(key);
+    if (gl) {
+        // groups of whole lanes, valued on the same grid: the two largest by exchanges
+        uint32_t top1 = key[0], top2 = N > 1 ? key[N > 1 ? 1 : 0] : 0u;
+        for (int o = 1; o < gl; o <<= 1) {
+            const uint32_t u1 = __shfl_xor_sync(0xffffffffu, top1, o), u2 = __shfl_xor_sync(0xffffffffu, top2, o);
+            top2 = max(min(top1, u1), max(top2, u2));
+            top1 = max(top1, u1);
+        }
+        top1 >>= kIdBits;
+        top2 >>= kIdBits;
+        // the sum is -inf where one of two is; + 1: 0 means no group
+        uint32_t v = 1u + (a.group_top == 1 ? top1 : top2 == 0u ? 0u : top1 + top2);
+        v = __shfl_sync(0xffffffffu, v, (lane * gl) & 31);
+        uint32_t last, first;
+        const uint32_t kept = pick_groups(a, lane < a.n_group ? v : 0u, last, first);
+        sure = first == 0u || last - first > (a.group_top == 2 ? 4u * gap_key : gap_key);
+        if (!((kept >> (lane / gl)) & 1u))
+#pragma unroll
+            for (int i = 0; i < N; ++i) key[i] = 0u;
+    }
+    uint32_t my_key = 0, before = 0, least = 0xffffffffu;        // least gap, in grid steps
+#pragma unroll 1
+    for (int j = 0; j < a.k; ++j) {
+        const uint32_t best = __reduce_max_sync(0xffffffffu, key[0]);
+        if (j > 0) least = min(least, (before >> kIdBits) - (best >> kIdBits));
         before = best;
-        if (j == a.k) break;
-        sure = sure && (best >> kIdBits) != 0u;                  // an expert that is switched off: exact ties
+        const bool mine = key[0] == best;
 #pragma unroll
-        for (int i = 0; i < N; ++i) key[i] = key[i] == best ? 0u : key[i];
-        if (lane == j) my_id = static_cast<int>(kIdMask - (best & kIdMask));
+        for (int i = 0; i + 1 < N; ++i) key[i] = mine ? key[i + 1] : key[i];
+        key[N - 1] = mine ? 0u : key[N - 1];
+        if (lane == j) my_key = best;
     }
-    return my_id;
+    // the gap behind the last slot (a missing candidate is behind everything), and
+    // no slot may be an expert that is switched off: those tie exactly
+    const uint32_t next = __reduce_max_sync(0xffffffffu, key[0]);
+    if (next != 0u) least = min(least, (before >> kIdBits) - (next >> kIdBits));
+    sure = sure && least > gap_key && (before >> kIdBits) != 0u;
+    return static_cast<int>(kIdMask - (my_key & kIdMask));
 }
 
 template <int N, typename L>
 __global__ void __launch_bounds__(kWarpsPerBlock * 32)
-route_scored_kernel(const RouterArgs a) {
+route_scored_kernel(const __grid_constant__ RouterArgs a) {
     extern __shared__ double by_all[];                           // [kWarpsPerBlock][E], only with groups
     griddep_launch_dependents();
     griddep_wait();
@@ -409,29 +491,25 @@ route_scored_kernel(const RouterArgs a) {
         x[i] = clean_logit(x[i]);
         m = fmaxf(m, x[i]);
     }
-    if (soft) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    }
+    if (soft) m = warp_max(m);
     double *by_s = by_all + static_cast<size_t>(warp) * a.E;
     const bool by_logit = a.bias == nullptr;
     int id;
-    uint32_t bits = 0xffffffffu;
     bool sure = true;
     if (by_logit && a.n_group == 1) {
-        id = select_logits<N>(a, x, bits);
+        id = select_logits<N>(a, x, 0xffffffffu);
     } else {
         float s[N], c[N];
-        float err = 0.f;
-        if (!by_logit || a.group_top == 2) err = scores_32<N>(a, x, m, s, c);
-        if (a.n_group > 1) {
-            if (err > 0.f)
-                bits = kept_experts<N>(a, c, err, reinterpret_cast<float *>(by_s), sure);
-            else
-                bits = kept_experts<N>(a, x, 0.f, reinterpret_cast<float *>(by_s), sure);    // exact
-        }
-        id = by_logit ? select_logits<N>(a, x, bits) : select_choices<N>(a, c, err, bits, sure);
-        if (!sure) id = select_64<N>(a, x, m, by_s);
+        float err = 0.f, lo = 0.f, hi = 0.f;
+        if (!by_logit || a.group_top == 2) err = scores_32<N>(a, x, m, s, c, lo, hi);
+        float *by32 = reinterpret_cast<float *>(by_s);
+        if (!by_logit)
+            id = select_choices<N>(a, c, err, lo, hi, by32, sure);
+        else if (a.group_top == 2)
+            id = select_logits<N>(a, x, kept_experts<N>(a, s, err, by32, sure));
+        else
+            id = select_logits<N>(a, x, kept_experts<N>(a, x, 0.f, by32, sure));         // exact
+        if (!sure) id = select_64<N, L>(a, row, m, by_s);
     }
     // The weight of slot j, in lane j. Renormalised, only ratios of scores count:
     // softmax takes them relative to the largest selected logit, and so does a
@@ -443,9 +521,7 @@ route_scored_kernel(const RouterArgs a) {
         l = clean_logit(load_logit(row + id));
         off = a.bias && !(a.bias[id] > -INFINITY);
     }
-    float lmax = off ? -INFINITY : l;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) lmax = fmaxf(lmax, __shfl_xor_sync(0xffffffffu, lmax, o));
+    const float lmax = warp_max(off ? -INFINITY : l);
     float s;
     if (soft && !a.renormalize) {
         float z = 0.f;
