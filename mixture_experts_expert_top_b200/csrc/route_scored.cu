@@ -39,7 +39,7 @@ struct RouterArgs {
     int32_t *ids;
     float *w;
     int vec;                                // rows and lanes' shares are 16-byte aligned
-    int group_lanes;                        // lanes that hold one group, a power of two; 0: groups end inside lanes
+    int group_shift;                        // log2 of the lanes that hold one group; -1: groups end inside lanes
 };
 
 __device__ __forceinline__ float load_logit(const float *p) { return *p; }
@@ -83,6 +83,20 @@ __device__ __forceinline__ float clean_logit(float x) { return fmaxf(x, -INFINIT
 __device__ __forceinline__ float warp_max(float v) {
     float r;
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// 1 / x within 2^-23 (relative), 0 for +inf; exp(x) within 2^-22 + 2^-23 |x|.
+// Both flush subnormals.
+__device__ __forceinline__ float fast_rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ float fast_exp(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.44269504f));
     return r;
 }
 
@@ -205,17 +219,10 @@ __device__ __noinline__ int select_64(const RouterArgs &a, const L *row, float m
     return my_id;
 }
 
-// Reciprocal within 1 ulp (2^-23 relative), 0 for +inf.
-__device__ __forceinline__ float fast_rcp(float x) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
 // fp32 scores s and choices c = s + b of the lane's experts (lane l: l*N ..
 // l*N+N-1), their smallest and largest value over the row, and a bound on |c -
-// its 64-bit value|. In units of u = 2^-24: __expf is within 2 + 1.173 |x| ulp,
-// (4 + 2.35 |x|) u; the reciprocal within 2u; adding b rounds by u |c|. A
+// its 64-bit value|. In units of u = 2^-24: the exponential is within (4 + 2
+// |x|) u; the reciprocal within 2u; adding b rounds by u |c|. A
 // sigmoid passes on (1 - s) of its exponential's error: below 1.6 u, since s (1
 // - s) <= 0.25 and s (1 - s) |x| <= 0.23; its sum 1 + e adds one and its
 // reciprocal two of s <= 1: 4.6. A softmax term has its argument's rounding,
@@ -232,7 +239,7 @@ __device__ __forceinline__ float scores_32(const RouterArgs &a, const float (&x)
         float z = 0.f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            s[i] = x[i] == m ? (m == -INFINITY ? 0.f : 1.f) : __expf(x[i] - m);
+            s[i] = x[i] == m ? (m == -INFINITY ? 0.f : 1.f) : fast_exp(x[i] - m);
             z += s[i];
         }
 #pragma unroll
@@ -243,7 +250,7 @@ __device__ __forceinline__ float scores_32(const RouterArgs &a, const float (&x)
         err = (N + 45.0f) * inv;
     } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) s[i] = fast_rcp(1.0f + __expf(-x[i]));
+        for (int i = 0; i < N; ++i) s[i] = fast_rcp(1.0f + fast_exp(-x[i]));
         err = 4.6f;
     }
     float b[N];
@@ -309,19 +316,19 @@ __device__ __forceinline__ uint32_t kept_experts(const RouterArgs &a, const floa
         top1 = fmaxf(top1, v);
     };
     uint32_t gk = 0;
-    const int gl = a.group_lanes;
-    if (gl) {
+    const int gs = a.group_shift;
+    if (gs >= 0) {
         // whole lanes per group: each group's two largest by exchanges inside its lanes
 #pragma unroll
         for (int i = 0; i < N; ++i) add(e0 + i < a.E ? by[i] : -INFINITY);
-        for (int o = 1; o < gl; o <<= 1) {
+        for (int o = 1; o < (1 << gs); o <<= 1) {
             const float u1 = __shfl_xor_sync(0xffffffffu, top1, o), u2 = __shfl_xor_sync(0xffffffffu, top2, o);
             top2 = fmaxf(fminf(top1, u1), fmaxf(top2, u2));
             top1 = fmaxf(top1, u1);
         }
         // group g's value moves to lane g
         const float mine = a.group_top == 2 ? top1 + top2 : top1;
-        const float g = __shfl_sync(0xffffffffu, mine, (lane * gl) & 31);
+        const float g = __shfl_sync(0xffffffffu, mine, (lane << gs) & 31);
         gk = lane < a.n_group ? logit_key(g) : 0u;
     } else {
 #pragma unroll
@@ -338,7 +345,7 @@ __device__ __forceinline__ uint32_t kept_experts(const RouterArgs &a, const floa
     const uint32_t kept = pick_groups(a, gk, last, first);
     // a sum of two: twice the error, and its own rounding below it
     if (err_by > 0.f) sure = apart(last, first, (a.group_top == 2 ? 8.0f : 2.0f) * err_by);
-    if (gl) return (kept >> (lane / gl)) & 1u ? 0xffffffffu : 0u;
+    if (gs >= 0) return (kept >> (lane >> gs)) & 1u ? 0xffffffffu : 0u;
 #pragma unroll
     for (int i = 0; i < N; ++i)
         if (e0 + i < a.E) bits |= ((kept >> ((e0 + i) / size)) & 1u) << i;
@@ -405,9 +412,9 @@ __device__ __forceinline__ int select_choices(const RouterArgs &a, const float (
     constexpr float kMagic = 8388608.0f + 1.0f;                  // 2^23: a grid value lands in the low mantissa bits
     const int lane = threadIdx.x & 31;
     const int e0 = lane * N;
-    const int gl = a.n_group > 1 ? a.group_lanes : 0;
+    const int gs = a.group_shift;
     uint32_t bits = 0xffffffffu;
-    if (a.n_group > 1 && !gl) bits = kept_experts<N>(a, c, err, by_s, sure);
+    if (a.n_group > 1 && gs < 0) bits = kept_experts<N>(a, c, err, by_s, sure);
     const float unit = kSteps / (hi - lo);
     const float gap = ceilf(2.0f * err * unit) + 8.0f;           // 2 err, and each key's 3 roundings
     // one value, an infinity, or a range that the grid does not resolve: not here
@@ -430,43 +437,49 @@ __device__ __forceinline__ int select_choices(const RouterArgs &a, const float (
 #pragma unroll
         for (int i = 0; i < N; ++i) key[i] = (bits >> i) & 1u ? key[i] : 0u;
     sort_keys<N>(key);
-    if (gl) {
+    if (a.n_group > 1 && gs >= 0) {
         // groups of whole lanes, valued on the same grid: the two largest by exchanges
         uint32_t top1 = key[0], top2 = N > 1 ? key[N > 1 ? 1 : 0] : 0u;
-        for (int o = 1; o < gl; o <<= 1) {
+        for (int o = 1; o < (1 << gs); o <<= 1) {
             const uint32_t u1 = __shfl_xor_sync(0xffffffffu, top1, o), u2 = __shfl_xor_sync(0xffffffffu, top2, o);
             top2 = max(min(top1, u1), max(top2, u2));
             top1 = max(top1, u1);
         }
         top1 >>= kIdBits;
         top2 >>= kIdBits;
-        // the sum is -inf where one of two is; + 1: 0 means no group
-        uint32_t v = 1u + (a.group_top == 1 ? top1 : top2 == 0u ? 0u : top1 + top2);
-        v = __shfl_sync(0xffffffffu, v, (lane * gl) & 31);
-        uint32_t last, first;
-        const uint32_t kept = pick_groups(a, lane < a.n_group ? v : 0u, last, first);
-        sure = first == 0u || last - first > (a.group_top == 2 ? 4u * gap_key : gap_key);
-        if (!((kept >> (lane / gl)) & 1u))
+        // the sum is -inf (0) where one of two is; below it the inverted group index, so
+        // that values differ. Lanes behind the last group are behind every group.
+        const uint32_t g = static_cast<uint32_t>(lane) >> gs;
+        uint32_t v = a.group_top == 1 ? top1 : top2 == 0u ? 0u : top1 + top2;
+        v = g < static_cast<uint32_t>(a.n_group) ? (v << 5) + (31u - g) + 1u : 0u;
+        int ahead = 0;
+#pragma unroll 4
+        for (int o = 1 << gs; o < 32; o += 1 << gs) ahead += __shfl_xor_sync(0xffffffffu, v, o) > v ? 1 : 0;
+        const bool kept = ahead < a.topk_group;
+        const uint32_t last = __reduce_min_sync(0xffffffffu, kept ? v : 0xffffffffu);
+        const uint32_t first = __reduce_max_sync(0xffffffffu, kept ? 0u : v);
+        sure = first == 0u || ((last - 1u) >> 5) - ((first - 1u) >> 5) > (a.group_top == 2 ? 4u * gap_key : gap_key);
+        if (!kept)
 #pragma unroll
             for (int i = 0; i < N; ++i) key[i] = 0u;
     }
-    uint32_t my_key = 0, before = 0, least = 0xffffffffu;        // least gap, in grid steps
-#pragma unroll 1
+    uint32_t my_key = 0;
+#pragma unroll 2
     for (int j = 0; j < a.k; ++j) {
         const uint32_t best = __reduce_max_sync(0xffffffffu, key[0]);
-        if (j > 0) least = min(least, (before >> kIdBits) - (best >> kIdBits));
-        before = best;
         const bool mine = key[0] == best;
 #pragma unroll
         for (int i = 0; i + 1 < N; ++i) key[i] = mine ? key[i + 1] : key[i];
         key[N - 1] = mine ? 0u : key[N - 1];
         if (lane == j) my_key = best;
     }
-    // the gap behind the last slot (a missing candidate is behind everything), and
-    // no slot may be an expert that is switched off: those tie exactly
-    const uint32_t next = __reduce_max_sync(0xffffffffu, key[0]);
-    if (next != 0u) least = min(least, (before >> kIdBits) - (next >> kIdBits));
-    sure = sure && least > gap_key && (before >> kIdBits) != 0u;
+    // the gap behind each slot, in grid steps (a missing candidate is behind
+    // everything), and no slot may be an expert that is switched off: those tie exactly
+    uint32_t next = __reduce_max_sync(0xffffffffu, key[0]);
+    const uint32_t after = __shfl_down_sync(0xffffffffu, my_key, 1);
+    if (lane + 1 < a.k) next = after;
+    const bool near = lane < a.k && ((next != 0u && (my_key >> kIdBits) - (next >> kIdBits) <= gap_key) || (my_key >> kIdBits) == 0u);
+    sure = sure && !__any_sync(0xffffffffu, near);
     return static_cast<int>(kIdMask - (my_key & kIdMask));
 }
 
@@ -534,14 +547,16 @@ route_scored_kernel(const __grid_constant__ RouterArgs a) {
     } else if (soft || (a.renormalize && lmax < -60.0f)) {
         s = l == lmax ? 1.0f : expf(l - lmax);
     } else {
-        s = 1.0f / (1.0f + expf(-l));
+        s = fast_rcp(1.0f + expf(-l));
     }
     if (off || l == -INFINITY || lane >= a.k) s = 0.f;
     float wt = s;
     if (a.renormalize) {
-        float sum = 0.f;
-        for (int j = 0; j < a.k; ++j) sum += __shfl_sync(0xffffffffu, s, j);      // slot order
-        wt = sum > 0.f ? s / sum : 0.f;
+        float sum = 0.f;                                             // slot order; lanes from k on add 0
+        for (int j = 0; j < a.k; j += 8)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum += __shfl_sync(0xffffffffu, s, j + i);
+        wt = sum > 0.f ? __fdiv_rn(s, sum) : 0.f;
     }
     wt *= a.scale;
     int out_id = id;
@@ -558,7 +573,9 @@ cudaError_t launch_n(RouterArgs a, cudaStream_t s) {
     a.vec = a.E % N == 0 && N * sizeof(L) % 16 == 0 && N % 4 == 0 && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 &&
             reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
     const int size = a.E / a.n_group, lanes = size / N;
-    a.group_lanes = size % N == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
+    a.group_shift = -1;
+    if (size % N == 0 && (lanes & (lanes - 1)) == 0)
+        for (a.group_shift = 0; (1 << a.group_shift) < lanes;) ++a.group_shift;
     const int blocks = (a.T + kWarpsPerBlock - 1) / kWarpsPerBlock;
     const size_t sm = a.n_group > 1 ? static_cast<size_t>(kWarpsPerBlock) * a.E * sizeof(double) : 0;
     return launch_pdl(route_scored_kernel<N, L>, dim3(blocks), dim3(kWarpsPerBlock * 32), sm, s, a);
