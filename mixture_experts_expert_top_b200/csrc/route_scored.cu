@@ -16,8 +16,11 @@
 // values: scores are formed in fp32 with a bound on their error, the selection
 // runs on them, and it stands if every gap that decided it (between
 // consecutive selected experts, to the first one left out, and between the
-// last group kept and the first one dropped) exceeds twice the bound. The few
-// rows where one does not are selected again from 64-bit scores (select_64).
+// last group kept and the first one dropped) exceeds twice the bound. Where one
+// does not (about 1 row in 1000 of 256 experts), the experts down to the next
+// such gap are ordered by their 64-bit values, one per lane (refine_64); where
+// that does not settle it either (groups that tie, experts that are switched
+// off), the whole row is (select_64).
 #include <math.h>
 
 #include "common.cuh"
@@ -219,6 +222,49 @@ __device__ __noinline__ int select_64(const RouterArgs &a, const L *row, float m
     return my_id;
 }
 
+// The order of `count` <= 32 candidates (lane j < count: expert id) by their
+// 64-bit choices. Returns slot j's expert in lane j. One exponential per lane
+// and a rank by comparison with the others: a fifth of select_64's latency,
+// which a single row would add to the whole launch.
+template <typename L>
+__device__ __noinline__ int refine_64(const RouterArgs &a, const L *row, float m, int id, int count) {
+    __shared__ int slot_s[kWarpsPerBlock][32];
+    const int lane = threadIdx.x & 31;
+    const bool soft = a.score == MOE_SCORE_SOFTMAX;
+    double sum = 0.0;
+    if (soft) {
+        for (int e = lane; e < a.E; e += 32) {
+            const float x = clean_logit(load_logit(row + e));
+            sum += x == m ? 1.0 : exp(static_cast<double>(x) - m);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    }
+    uint64_t key = 0;
+    if (lane < count) {
+        const float x = clean_logit(load_logit(row + id));
+        double s;
+        if (soft)
+            s = (x == m ? 1.0 : exp(static_cast<double>(x) - m)) / sum;
+        else
+            s = 1.0 / (1.0 + exp(-static_cast<double>(x)));
+        key = choice_key(s + static_cast<double>(a.bias[id]));
+    }
+    int rank = 0;
+#pragma unroll 4
+    for (int o = 0; o < count; ++o) {
+        const uint64_t other = __shfl_sync(0xffffffffu, key, o);
+        const int oid = __shfl_sync(0xffffffffu, id, o);
+        rank += other > key || (other == key && oid < id) ? 1 : 0;
+    }
+    int *slots = slot_s[threadIdx.x >> 5];
+    if (lane < count) slots[rank] = id;
+    __syncwarp();
+    const int mine = lane < a.k ? slots[lane] : 0;
+    __syncwarp();
+    return mine;
+}
+
 // fp32 scores s and choices c = s + b of the lane's experts (lane l: l*N ..
 // l*N+N-1), their smallest and largest value over the row, and a bound on |c -
 // its 64-bit value|. In units of u = 2^-24: the exponential is within (4 + 2
@@ -401,11 +447,13 @@ __device__ __forceinline__ void sort_keys(uint32_t (&key)[N]) {
 // from the smallest finite choice lo to the largest, hi, above the inverted
 // expert id, so keys differ: each lane sorts its own once (minima and maxima
 // only), and a slot takes one reduction over the lanes' largest. Grid value 0
-// is an expert that is switched off. `sure` stays true if every gap is beyond
-// the errors and the grid. Returns slot j's expert in lane j.
+// is an expert that is switched off. Returns slot j's expert in lane j, and in
+// `count`: 0 if the 64-bit selection is the same, every gap being beyond the
+// errors and the grid; c > 0 if the first c candidates (in lanes 0 .. c-1)
+// hold it, but not surely in this order; -1 if it may be anywhere.
 template <int N>
 __device__ __forceinline__ int select_choices(const RouterArgs &a, const float (&c)[N], float err, float lo, float hi,
-                                              float *by_s, bool &sure) {
+                                              float *by_s, int &count) {
     constexpr int kIdBits = N <= 16 ? 9 : 10;
     constexpr uint32_t kIdMask = (1u << kIdBits) - 1u;
     constexpr float kSteps = static_cast<float>((1u << (32 - kIdBits)) - 4u);
@@ -414,6 +462,8 @@ __device__ __forceinline__ int select_choices(const RouterArgs &a, const float (
     const int e0 = lane * N;
     const int gs = a.group_shift;
     uint32_t bits = 0xffffffffu;
+    bool sure = true;
+    count = -1;
     if (a.n_group > 1 && gs < 0) bits = kept_experts<N>(a, c, err, by_s, sure);
     const float unit = kSteps / (hi - lo);
     const float gap = ceilf(2.0f * err * unit) + 8.0f;           // 2 err, and each key's 3 roundings
@@ -464,22 +514,40 @@ __device__ __forceinline__ int select_choices(const RouterArgs &a, const float (
             for (int i = 0; i < N; ++i) key[i] = 0u;
     }
     uint32_t my_key = 0;
-#pragma unroll 2
-    for (int j = 0; j < a.k; ++j) {
-        const uint32_t best = __reduce_max_sync(0xffffffffu, key[0]);
+    auto pop = [&](uint32_t best) {
         const bool mine = key[0] == best;
 #pragma unroll
         for (int i = 0; i + 1 < N; ++i) key[i] = mine ? key[i + 1] : key[i];
         key[N - 1] = mine ? 0u : key[N - 1];
+    };
+#pragma unroll 2
+    for (int j = 0; j < a.k; ++j) {
+        const uint32_t best = __reduce_max_sync(0xffffffffu, key[0]);
+        pop(best);
         if (lane == j) my_key = best;
     }
     // the gap behind each slot, in grid steps (a missing candidate is behind
-    // everything), and no slot may be an expert that is switched off: those tie exactly
+    // everything); an expert that is switched off (grid value 0) ties exactly
+    auto near = [&](uint32_t k0, uint32_t k1) { return k1 != 0u && (k0 >> kIdBits) - (k1 >> kIdBits) <= gap_key; };
     uint32_t next = __reduce_max_sync(0xffffffffu, key[0]);
     const uint32_t after = __shfl_down_sync(0xffffffffu, my_key, 1);
-    if (lane + 1 < a.k) next = after;
-    const bool near = lane < a.k && ((next != 0u && (my_key >> kIdBits) - (next >> kIdBits) <= gap_key) || (my_key >> kIdBits) == 0u);
-    sure = sure && !__any_sync(0xffffffffu, near);
+    const uint32_t behind = lane + 1 < a.k ? after : next;
+    const bool off = __any_sync(0xffffffffu, lane < a.k && (my_key >> kIdBits) == 0u);
+    if (!__any_sync(0xffffffffu, lane < a.k && near(my_key, behind)) && sure && !off) {
+        count = 0;
+    } else if (sure && !off) {
+        // candidates down to a gap
+        uint32_t last = __shfl_sync(0xffffffffu, my_key, a.k - 1);
+        int n = a.k;
+        while (n < 32 && near(last, next)) {
+            pop(next);
+            if (lane == n) my_key = next;
+            ++n;
+            last = next;
+            next = __reduce_max_sync(0xffffffffu, key[0]);
+        }
+        if (!near(last, next) && (last >> kIdBits) != 0u) count = n;
+    }
     return static_cast<int>(kIdMask - (my_key & kIdMask));
 }
 
@@ -516,9 +584,12 @@ route_scored_kernel(const __grid_constant__ RouterArgs a) {
         float err = 0.f, lo = 0.f, hi = 0.f;
         if (!by_logit || a.group_top == 2) err = scores_32<N>(a, x, m, s, c, lo, hi);
         float *by32 = reinterpret_cast<float *>(by_s);
-        if (!by_logit)
-            id = select_choices<N>(a, c, err, lo, hi, by32, sure);
-        else if (a.group_top == 2)
+        if (!by_logit) {
+            int count;
+            id = select_choices<N>(a, c, err, lo, hi, by32, count);
+            sure = count >= 0;
+            if (count > 0) id = refine_64<L>(a, row, m, id, count);
+        } else if (a.group_top == 2)
             id = select_logits<N>(a, x, kept_experts<N>(a, s, err, by32, sure));
         else
             id = select_logits<N>(a, x, kept_experts<N>(a, x, 0.f, by32, sure));         // exact
