@@ -140,69 +140,91 @@ __device__ __forceinline__ uint32_t keep_groups(Key mine, int n_group, int keep)
     return __ballot_sync(0xffffffffu, lane < n_group && ahead < keep);
 }
 
-// The selection in 64 bits. Lane l holds experts l*N .. l*N+N-1. Returns slot
-// j's expert in lane j. It reads its logits again, so that the callers that
-// rarely need it keep theirs in registers.
+// 64-bit scores of the lane's experts (lane l: l*N .. l*N+N-1). The logits are
+// read again, so that callers that rarely come here keep theirs in registers.
+// No branch between the exponentials: their latencies overlap.
 template <int N, typename L>
-__device__ __noinline__ int select_64(const RouterArgs &a, const L *row, float m, double *by_s) {
-    const int lane = threadIdx.x & 31;
-    const int e0 = lane * N;
+__device__ __forceinline__ void scores_64(const RouterArgs &a, const L *row, float m, double (&s)[N]) {
+    const int e0 = (threadIdx.x & 31) * N;
     float x[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = e0 + i < a.E ? clean_logit(load_logit(row + e0 + i)) : -INFINITY;
-    const bool soft = a.score == MOE_SCORE_SOFTMAX;
-    const bool by_logit = a.bias == nullptr;                     // experts are ordered by their logits
-    const bool groups_by_logit = by_logit && a.group_top == 1;
-    double s[N];
-    const bool need_scores = !by_logit || (a.n_group > 1 && !groups_by_logit);
-    double sum = 0.0;
+    if (a.score == MOE_SCORE_SOFTMAX) {
+        double sum = 0.0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        s[i] = 0.0;
-        if (need_scores && e0 + i < a.E) {
-            if (soft)
-                s[i] = x[i] == m ? (m == -INFINITY ? 0.0 : 1.0) : exp(static_cast<double>(x[i]) - m);
-            else
-                s[i] = 1.0 / (1.0 + exp(-static_cast<double>(x[i])));
+        for (int i = 0; i < N; ++i) {
+            s[i] = x[i] == m ? (m == -INFINITY ? 0.0 : 1.0) : exp(static_cast<double>(x[i]) - m);
             sum += s[i];
         }
-    }
-    if (need_scores && soft) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
 #pragma unroll
         for (int i = 0; i < N; ++i)
             if (sum > 0.0) s[i] /= sum;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[i] = exp(-static_cast<double>(x[i]));
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[i] = 1.0 / (1.0 + s[i]);
     }
-    uint64_t key[N];
+}
+
+// Whether each of the lane's experts is in a kept group, as bits, by 64-bit
+// group values: sums of the group_top largest choices (scores without a bias).
+template <int N, typename L>
+__device__ __noinline__ uint32_t groups_64(const RouterArgs &a, const L *row, float m, double *by_s) {
+    const int lane = threadIdx.x & 31;
+    const int e0 = lane * N;
+    const int size = a.E / a.n_group, gs = a.group_shift;
+    double by[N];
+    scores_64<N>(a, row, m, by);
+    double top1 = -INFINITY, top2 = -INFINITY;
+    auto add = [&](double v) {
+        if (v > top1) { top2 = top1; top1 = v; }
+        else if (v > top2) top2 = v;                             // NaN is never larger: it counts as -inf
+    };
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        key[i] = 0;
         if (e0 + i < a.E) {
-            const double c = by_logit ? static_cast<double>(x[i]) : s[i] + static_cast<double>(a.bias[e0 + i]);
-            key[i] = choice_key(c);
-            if (a.n_group > 1) by_s[e0 + i] = by_logit && !groups_by_logit ? s[i] : c;
+            if (a.bias) by[i] += static_cast<double>(a.bias[e0 + i]);
+            if (gs >= 0) add(by[i]); else by_s[e0 + i] = by[i];
         }
     }
-    if (a.n_group > 1) {
+    if (gs >= 0) {
+        for (int o = 1; o < (1 << gs); o <<= 1) {
+            const double u1 = __shfl_xor_sync(0xffffffffu, top1, o), u2 = __shfl_xor_sync(0xffffffffu, top2, o);
+            top2 = fmax(fmin(top1, u1), fmax(top2, u2));
+            top1 = fmax(top1, u1);
+        }
+        top1 = __shfl_sync(0xffffffffu, top1, (lane << gs) & 31);
+        top2 = __shfl_sync(0xffffffffu, top2, (lane << gs) & 31);
+    } else {
         __syncwarp();
-        const int size = a.E / a.n_group;
-        uint64_t gk = 0;
-        if (lane < a.n_group) {
-            double top1 = -INFINITY, top2 = -INFINITY;
-            for (int i = 0; i < size; ++i) {
-                double v = by_s[lane * size + i];
-                if (v != v) v = -INFINITY;
-                if (v > top1) { top2 = top1; top1 = v; }
-                else if (v > top2) top2 = v;
-            }
-            gk = choice_key(a.group_top == 2 ? top1 + top2 : top1);
-        }
-        const uint32_t kept = keep_groups(gk, a.n_group, a.topk_group);
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (e0 + i < a.E && !((kept >> ((e0 + i) / size)) & 1u)) key[i] = 0;
+        if (lane < a.n_group)
+            for (int i = 0; i < size; ++i) add(by_s[lane * size + i]);
+        __syncwarp();
     }
+    const uint64_t gk = lane < a.n_group ? choice_key(a.group_top == 2 ? top1 + top2 : top1) : 0;
+    const uint32_t kept = keep_groups(gk, a.n_group, a.topk_group);
+    uint32_t bits = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (e0 + i < a.E) bits |= ((kept >> ((e0 + i) / size)) & 1u) << i;
+    return bits;
+}
+
+// The selection in 64 bits among the lane's experts in `bits`. Returns slot j's
+// expert in lane j. Only with a bias: without one the logits decide.
+template <int N, typename L>
+__device__ __noinline__ int select_64(const RouterArgs &a, const L *row, float m, uint32_t bits) {
+    const int lane = threadIdx.x & 31;
+    const int e0 = lane * N;
+    double s[N];
+    scores_64<N>(a, row, m, s);
+    uint64_t key[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        key[i] = e0 + i < a.E && ((bits >> i) & 1u) ? choice_key(s[i] + static_cast<double>(a.bias[e0 + i])) : 0;
     int my_id = 0;
     for (int j = 0; j < a.k; ++j) {
         uint64_t local = 0;
@@ -224,7 +246,7 @@ __device__ __noinline__ int select_64(const RouterArgs &a, const L *row, float m
 
 // The order of `count` <= 32 candidates (lane j < count: expert id) by their
 // 64-bit choices. Returns slot j's expert in lane j. One exponential per lane
-// and a rank by comparison with the others: a fifth of select_64's latency,
+// and a rank by comparison with the others: a fraction of select_64's latency,
 // which a single row would add to the whole launch.
 template <typename L>
 __device__ __noinline__ int refine_64(const RouterArgs &a, const L *row, float m, int id, int count) {
@@ -450,10 +472,12 @@ __device__ __forceinline__ void sort_keys(uint32_t (&key)[N]) {
 // is an expert that is switched off. Returns slot j's expert in lane j, and in
 // `count`: 0 if the 64-bit selection is the same, every gap being beyond the
 // errors and the grid; c > 0 if the first c candidates (in lanes 0 .. c-1)
-// hold it, but not surely in this order; -1 if it may be anywhere.
-template <int N>
-__device__ __forceinline__ int select_choices(const RouterArgs &a, const float (&c)[N], float err, float lo, float hi,
-                                              float *by_s, int &count) {
+// hold it, but not surely in this order; -1 if it may be anywhere in `bits`,
+// the lane's experts in kept groups. Groups that are too near are valued in 64
+// bits on the way.
+template <int N, typename L>
+__device__ __forceinline__ int select_choices(const RouterArgs &a, const L *row, float m, const float (&c)[N], float err,
+                                              float lo, float hi, double *by_s, int &count, uint32_t &bits) {
     constexpr int kIdBits = N <= 16 ? 9 : 10;
     constexpr uint32_t kIdMask = (1u << kIdBits) - 1u;
     constexpr float kSteps = static_cast<float>((1u << (32 - kIdBits)) - 4u);
@@ -461,15 +485,19 @@ __device__ __forceinline__ int select_choices(const RouterArgs &a, const float (
     const int lane = threadIdx.x & 31;
     const int e0 = lane * N;
     const int gs = a.group_shift;
-    uint32_t bits = 0xffffffffu;
-    bool sure = true;
+    bits = 0xffffffffu;
     count = -1;
-    if (a.n_group > 1 && gs < 0) bits = kept_experts<N>(a, c, err, by_s, sure);
     const float unit = kSteps / (hi - lo);
-    const float gap = ceilf(2.0f * err * unit) + 8.0f;           // 2 err, and each key's 3 roundings
+    // twice the error and the two keys' rounding, one step each
+    const float gap = ceilf(2.0f * err * unit) + 3.0f;
     // one value, an infinity, or a range that the grid does not resolve: not here
-    sure = sure && lo < hi && hi < INFINITY && unit < 3e37f && gap < kSteps;
-    if (!sure) return 0;
+    const bool grid_ok = lo < hi && hi < INFINITY && unit < 3e37f && gap < 0.125f * kSteps;
+    if (a.n_group > 1 && (gs < 0 || !grid_ok)) {
+        bool sure = true;
+        bits = kept_experts<N>(a, c, err, reinterpret_cast<float *>(by_s), sure);
+        if (!sure) bits = groups_64<N, L>(a, row, m, by_s);
+    }
+    if (!grid_ok) return 0;
     const uint32_t gap_key = static_cast<uint32_t>(gap);
     uint32_t key[N];
 #pragma unroll
@@ -508,8 +536,11 @@ __device__ __forceinline__ int select_choices(const RouterArgs &a, const float (
         const bool kept = ahead < a.topk_group;
         const uint32_t last = __reduce_min_sync(0xffffffffu, kept ? v : 0xffffffffu);
         const uint32_t first = __reduce_max_sync(0xffffffffu, kept ? 0u : v);
-        sure = first == 0u || ((last - 1u) >> 5) - ((first - 1u) >> 5) > (a.group_top == 2 ? 4u * gap_key : gap_key);
-        if (!kept)
+        bits = kept ? 0xffffffffu : 0u;
+        // a sum of two: twice the error, its own rounding below it, and twice the steps
+        if (first != 0u && ((last - 1u) >> 5) - ((first - 1u) >> 5) <= (a.group_top == 2 ? 4u * gap_key : gap_key))
+            bits = groups_64<N, L>(a, row, m, by_s);
+        if (!bits)
 #pragma unroll
             for (int i = 0; i < N; ++i) key[i] = 0u;
     }
@@ -533,9 +564,9 @@ __device__ __forceinline__ int select_choices(const RouterArgs &a, const float (
     const uint32_t after = __shfl_down_sync(0xffffffffu, my_key, 1);
     const uint32_t behind = lane + 1 < a.k ? after : next;
     const bool off = __any_sync(0xffffffffu, lane < a.k && (my_key >> kIdBits) == 0u);
-    if (!__any_sync(0xffffffffu, lane < a.k && near(my_key, behind)) && sure && !off) {
+    if (!off && !__any_sync(0xffffffffu, lane < a.k && near(my_key, behind))) {
         count = 0;
-    } else if (sure && !off) {
+    } else if (!off) {
         // candidates down to a gap
         uint32_t last = __shfl_sync(0xffffffffu, my_key, a.k - 1);
         int n = a.k;
@@ -576,24 +607,26 @@ route_scored_kernel(const __grid_constant__ RouterArgs a) {
     double *by_s = by_all + static_cast<size_t>(warp) * a.E;
     const bool by_logit = a.bias == nullptr;
     int id;
-    bool sure = true;
     if (by_logit && a.n_group == 1) {
         id = select_logits<N>(a, x, 0xffffffffu);
+    } else if (by_logit && a.group_top == 1) {
+        bool sure = true;
+        id = select_logits<N>(a, x, kept_experts<N>(a, x, 0.f, reinterpret_cast<float *>(by_s), sure));      // exact
     } else {
-        float s[N], c[N];
-        float err = 0.f, lo = 0.f, hi = 0.f;
-        if (!by_logit || a.group_top == 2) err = scores_32<N>(a, x, m, s, c, lo, hi);
-        float *by32 = reinterpret_cast<float *>(by_s);
-        if (!by_logit) {
+        float s[N], c[N], lo, hi;
+        const float err = scores_32<N>(a, x, m, s, c, lo, hi);
+        if (by_logit) {
+            bool sure = true;
+            uint32_t bits = kept_experts<N>(a, s, err, reinterpret_cast<float *>(by_s), sure);
+            if (!sure) bits = groups_64<N, L>(a, row, m, by_s);
+            id = select_logits<N>(a, x, bits);
+        } else {
             int count;
-            id = select_choices<N>(a, c, err, lo, hi, by32, count);
-            sure = count >= 0;
+            uint32_t bits;
+            id = select_choices<N, L>(a, row, m, c, err, lo, hi, by_s, count, bits);
             if (count > 0) id = refine_64<L>(a, row, m, id, count);
-        } else if (a.group_top == 2)
-            id = select_logits<N>(a, x, kept_experts<N>(a, s, err, by32, sure));
-        else
-            id = select_logits<N>(a, x, kept_experts<N>(a, x, 0.f, by32, sure));         // exact
-        if (!sure) id = select_64<N, L>(a, row, m, by_s);
+            if (count < 0) id = select_64<N, L>(a, row, m, bits);
+        }
     }
     // The weight of slot j, in lane j. Renormalised, only ratios of scores count:
     // softmax takes them relative to the largest selected logit, and so does a
