@@ -261,6 +261,12 @@ bool gemm_i8_gathers_in_kernel(int P, int E) { return static_cast<double>(P) / E
 cudaError_t launch_grouped_gemm_i8(const I8GemmArgs &g, cudaStream_t s) {
     if (g.base.P == 0) return cudaSuccess;
     const double avg = static_cast<double>(g.base.P) / g.base.E;
+    // Few rows in all: latency counts, and reading weights into registers starts
+    // sooner. Measured against the tensor-core kernel (us, gate/up and down of
+    // 2048 x 768, 128 experts): 8 rows 6.0 / 11.7 and 3.6 / 5.9, 32 rows 20.1 /
+    // 22.8 and 13.3 / 13.7, 64 rows 33.4 / 31.7 and 21.6 / 19.3. Past 4 rows per
+    // expert the weights pass more than once (2 experts, 16 rows: 7.1 / 6.4).
+    if (g.base.P <= 32 && avg <= 4) return launch_grouped_gemm_i8_rows(g, s);
     if (!g.base.perm && avg > 48) return launch_grouped_gemm_i8_pair(g, s);
     if (g.base.swiglu) {
         if (avg <= 24) return run_i8<32, 5, true>(g, s);
