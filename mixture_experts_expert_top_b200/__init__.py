@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -229,20 +230,34 @@ def _pd(t, n: int, dtype, dev: int) -> Optional[int]:
     raise ValueError(f"libmoe_b200: expected a tensor on the current CUDA device, got one on {t.device}")
 
 
+_cuda_used = False
+
+
 def _dev() -> int:
     """Index of the current CUDA device (-2 while this process has not used CUDA:
     then no tensor is on one)."""
-    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+    global _cuda_used
+    if not _cuda_used:
+        _cuda_used = torch.cuda.is_initialized()
+        if not _cuda_used:
+            return -2
+    return torch._C._cuda_getDevice()
 
 
-def _s(stream) -> Optional[int]:
+def _s(stream, dev: Optional[int] = None) -> Optional[int]:
+    """A stream's handle; None is the current stream (of device dev, the current
+    one). torch.cuda.current_stream() would build a Stream object, which takes
+    longer (3.3 us) than a kernel's launch."""
     if stream is None:
-        # the handle of torch.cuda.current_stream() without building the Stream object,
-        # which takes longer (3.3 us) than a kernel's launch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if dev is None or dev < 0 else dev)
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
+
+
+def _dims(shape: Shape):
+    """(T, H, I, E, top_k, fmt, n_shared) of a shape."""
+    return struct.unpack_from("7i", shape)
 
 
 def _check(status: int, where: str) -> None:
@@ -278,10 +293,10 @@ def moe_route(logits, shape, topk_ids, topk_w, stream=None) -> None:
 
 def moe_route_scored(logits, bias, router: Router, shape, topk_ids, topk_w, stream=None) -> None:
     sh, d = _shape(shape), _dev()
-    T, E = sh.T, sh.E
-    n = T * sh.slots
+    T, _, _, E, k, _, S = _dims(sh)
+    n = T * (k + S)
     _check(lib().moe_route_scored(_pd(logits, T * E, BF16 if router.logits else F32, d), _pd(bias, E, F32, d),
-                                  router, sh, _pd(topk_ids, n, I32, d), _pd(topk_w, n, F32, d), _s(stream)),
+                                  router, sh, _pd(topk_ids, n, I32, d), _pd(topk_w, n, F32, d), _s(stream, d)),
            "moe_route_scored")
 
 
@@ -293,7 +308,7 @@ def moe_rmsnorm(x, residual, weight, eps: float, rows: int, H: int, fmt, residua
     else:
         q_p, s_p = _pd(q, n, U8, d), _pd(scales, n // 32, U8, d)
     _check(lib().moe_rmsnorm(_pd(x, n, BF16, d), _pd(residual, n, BF16, d), _pd(weight, H, BF16, d), eps, rows, H, fmt,
-                             _pd(residual_out, n, BF16, d), _pd(y, n, BF16, d), q_p, s_p, _s(stream)),
+                             _pd(residual_out, n, BF16, d), _pd(y, n, BF16, d), q_p, s_p, _s(stream, d)),
            "moe_rmsnorm")
 
 
@@ -382,27 +397,29 @@ def moe_grouped_gemm_down_mx(act_q, act_scales, offsets, w_d, w_d_scales, shape,
 def moe_i8_quantize(x, rows: int, K: int, q, scales, stream=None) -> None:
     n, d = rows * K, _dev()
     _check(lib().moe_i8_quantize(_pd(x, n, BF16, d), rows, K, _pd(q, n, I8, d), _pd(scales, rows, F32, d),
-                                 _s(stream)),
+                                 _s(stream, d)),
            "moe_i8_quantize")
 
 
 def moe_grouped_gemm_swiglu_i8(a_q, a_scales, perm, offsets, w_gu, w_gu_scales, shape, act, stream=None) -> None:
     sh, d = _shape(shape), _dev()
-    P, E, H, I = sh.T * sh.slots, sh.experts, sh.H, sh.I
-    rows = P if perm is None else sh.T
+    T, H, I, E, k, _, S = _dims(sh)
+    P, E = T * (k + S), E + S
+    rows = P if perm is None else T
     _check(lib().moe_grouped_gemm_swiglu_i8(_pd(a_q, rows * H, I8, d), _pd(a_scales, rows, F32, d),
                                             _pd(perm, P, I32, d), _pd(offsets, E + 1, I32, d),
                                             _pd(w_gu, E * 2 * I * H, I8, d), _pd(w_gu_scales, E * 2 * I, F32, d), sh,
-                                            _pd(act, P * I, BF16, d), _s(stream)),
+                                            _pd(act, P * I, BF16, d), _s(stream, d)),
            "moe_grouped_gemm_swiglu_i8")
 
 
 def moe_grouped_gemm_down_i8(act_q, act_scales, offsets, w_d, w_d_scales, shape, y, stream=None) -> None:
     sh, d = _shape(shape), _dev()
-    P, E, H, I = sh.T * sh.slots, sh.experts, sh.H, sh.I
+    T, H, I, E, k, _, S = _dims(sh)
+    P, E = T * (k + S), E + S
     _check(lib().moe_grouped_gemm_down_i8(_pd(act_q, P * I, I8, d), _pd(act_scales, P, F32, d),
                                           _pd(offsets, E + 1, I32, d), _pd(w_d, E * H * I, I8, d),
-                                          _pd(w_d_scales, E * H, F32, d), sh, _pd(y, P * H, BF16, d), _s(stream)),
+                                          _pd(w_d_scales, E * H, F32, d), sh, _pd(y, P * H, BF16, d), _s(stream, d)),
            "moe_grouped_gemm_down_i8")
 
 
@@ -424,7 +441,7 @@ def moe_forward_scored(hidden, logits, bias, router: Router, w_gu, w_gu_scales, 
                                     _pd(bias, sh.E, F32, d), router, _pd(w_gu, E * 2 * I * codes(H), w_dt, d),
                                     _pd(w_gu_scales, E * 2 * I * scales(H), s_dt, d),
                                     _pd(w_d, E * H * codes(I), w_dt, d), _pd(w_d_scales, E * H * scales(I), s_dt, d),
-                                    sh, _pd(out, T * H, BF16, d), _pd(ws, 0, ws.dtype, d), nbytes, _s(stream)),
+                                    sh, _pd(out, T * H, BF16, d), _pd(ws, 0, ws.dtype, d), nbytes, _s(stream, d)),
            "moe_forward_scored")
 
 
