@@ -217,6 +217,16 @@ __device__ __forceinline__ void tma_load_5d_pair(void *dst, const CUtensorMap *m
         : "memory");
 }
 
+// 5-D tiled load by one CTA (coordinates innermost first).
+__device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int c1, int c2,
+                                            int c3, int c4, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "l"(policy)
+        : "memory");
+}
+
 // Four-row gather: rows r0..r3 (any rows of the tensor), K columns x..x+box-1
 // each, land as four consecutive rows at dst. The tensor map's box must be
 // one row high.
@@ -491,28 +501,6 @@ __host__ __device__ __forceinline__ uint32_t idesc_i8_i32(int M, int N) {
            | (1u << 10)                                     // B format: s8
            | (static_cast<uint32_t>(N >> 3) << 17)          // N >> 3
            | (static_cast<uint32_t>(M >> 4) << 24);         // M >> 4
-}
-
-// D[tmem] (+)= A[smem] * B[smem]^T, K = 32 per instruction, one CTA.
-__device__ __forceinline__ void umma_i8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                           uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
-// The CTA-pair form, issued by the leading CTA only (operands as umma_bf16_ss_pair's).
-__device__ __forceinline__ void umma_i8_ss_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                                uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
 }
 
 // ----------------------------------------------------------------- numerics --

@@ -58,6 +58,118 @@ inline bool make_gate_up_map(CUtensorMap *m, const void *w, uint64_t E, uint64_t
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The tiles of a CTA (or pair) in order, for a converged warp: every 32 tiles
+// each lane decodes one of them (a search over the experts and two divisions,
+// about 800 cycles), and each tile is then a few shuffles. Tiles have up to
+// BLOCK token rows; the instruction's N is their number rounded up to STEP.
+template <int BLOCK, int STEP>
+struct TileFeed {
+    const int *pre, *off;
+    int E, MB, tile, step, total, left;
+    TileInfo mine;
+
+    __device__ __forceinline__ TileFeed(const int *pre_, const int *off_, int E_, int MB_, int first, int step_)
+        : pre(pre_), off(off_), E(E_), MB(MB_), tile(first), step(step_), total(pre_[E_]), left(0) {}
+
+    // False when there is none left.
+    __device__ __forceinline__ bool next(TileInfo &t) {
+        if (tile >= total) return false;
+        if (left == 0) {
+            const int lane = threadIdx.x & 31;
+            const long long at = tile + static_cast<long long>(lane) * step;
+            mine = decode_tile(at < total ? static_cast<int>(at) : tile, pre, off, E, MB, BLOCK);
+            left = 32;
+        }
+        const int src = 32 - left;
+        t.e = __shfl_sync(0xffffffffu, mine.e, src);
+        t.mb = __shfl_sync(0xffffffffu, mine.mb, src);
+        t.row0 = __shfl_sync(0xffffffffu, mine.row0, src);
+        t.valid = __shfl_sync(0xffffffffu, mine.valid, src);
+        t.n_mma = (t.valid + STEP - 1) & ~(STEP - 1);
+        --left;
+        tile += step;
+        return true;
+    }
+};
+
+// Weight scales of this thread's accumulator rows in the fragment layout of
+// tmem_ld_16x256b_x4: rows lane / 4 + 8 i of the warp's 32 (gate/up: i = 0, 1 gate
+// rows, 2, 3 the matching up rows). f0: the warp's first feature.
+template <bool SWIGLU>
+__device__ __forceinline__ void i8_weight_scales(const I8Params &ip, int e, int f0, float (&sw)[4]) {
+    const Params &p = ip.p;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int f = f0 + ((threadIdx.x & 31) >> 2) + 8 * (SWIGLU ? i & 1 : i);
+        const size_t row = static_cast<size_t>(e) * p.w_rows + f + (SWIGLU && i >= 2 ? p.m_out : 0);
+        sw[i] = f < p.m_out ? __ldg(ip.w_sf + row) : 0.f;
+    }
+}
+
+// Epilogue of 32 tokens by one warp: its 32 accumulator lanes (a: lanes 0-15, b:
+// lanes 16-31, tmem_ld_16x256b_x4) scaled, for gate/up combined (lanes 0-15 are
+// gate rows, 16-31 the up rows of the same features), rounded to bf16 pairs,
+// transposed by stmatrix into rows of tokens in shared memory and stored 16
+// bytes at a time.
+template <bool SWIGLU>
+struct I8RowWriter {
+    static constexpr int kFeat = SWIGLU ? 16 : 32;               // features of a warp
+    static constexpr int kPieces = kFeat / 8;                    // 16-byte pieces of its token rows
+    // 16 bytes of padding keep the eight rows of a stmatrix on different banks
+    static constexpr int kRowBytes = 2 * kFeat + 16;
+    static constexpr int kBytes = 32 * kRowBytes;                // shared memory per warp
+    uint8_t *rows;
+    uint32_t st_addr;
+
+    __device__ __forceinline__ explicit I8RowWriter(uint8_t *rows_) : rows(rows_) {
+        // this lane's row address of a stmatrix: matrix lane / 8 is 8 features (down) or,
+        // gate/up, 8 features of token group lane / 16
+        const int lane = threadIdx.x & 31;
+        st_addr = smem_u32(rows) + (SWIGLU ? ((lane >> 4) * 8 + (lane & 7)) * kRowBytes + ((lane >> 3) & 1) * 16
+                                           : (lane & 7) * kRowBytes + (lane >> 3) * 16);
+    }
+
+    // sx: the 32 tokens' scales in shared memory; f0: the warp's first feature;
+    // row0: the first token's output row, of which `valid` are the tile's.
+    __device__ __forceinline__ void write(const Params &p, const uint32_t (&a)[16], const uint32_t (&b)[16],
+                                          const float (&sw)[4], const float *sx, int f0, int row0, int valid) const {
+        const int lane = threadIdx.x & 31;
+        sx += 2 * (lane & 3);
+        uint32_t lo[4], hi[4];                                   // gate/up: features 0-7, 8-15 of each token group
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const float2 s = *reinterpret_cast<const float2 *>(sx + 8 * g);
+            float v[8];                                          // [row lane / 4 + 8 i][token 0, 1]
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t *r = i < 2 ? a + 4 * g + 2 * i : b + 4 * g + 2 * (i - 2);
+                v[2 * i] = i8_scaled(r[0], sw[i], s.x);
+                v[2 * i + 1] = i8_scaled(r[1], sw[i], s.y);
+            }
+            if constexpr (SWIGLU) {
+                lo[g] = i8_bf16x2(i8_act(v[0], v[4]), i8_act(v[1], v[5]));
+                hi[g] = i8_bf16x2(i8_act(v[2], v[6]), i8_act(v[3], v[7]));
+                if (g & 1) stmatrix_x4_trans(st_addr + 8 * (g - 1) * kRowBytes, lo[g - 1], hi[g - 1], lo[g], hi[g]);
+            } else {
+                stmatrix_x4_trans(st_addr + 8 * g * kRowBytes, i8_bf16x2(v[0], v[1]), i8_bf16x2(v[2], v[3]),
+                                  i8_bf16x2(v[4], v[5]), i8_bf16x2(v[6], v[7]));
+            }
+        }
+        __syncwarp();
+        const int piece = lane % kPieces;
+        if (f0 + 8 * piece < p.m_out) {
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                const int t = lane / kPieces + i * (32 / kPieces);
+                const uint4 v = *reinterpret_cast<const uint4 *>(rows + t * kRowBytes + 16 * piece);
+                if (t < valid)
+                    *reinterpret_cast<uint4 *>(p.out + static_cast<size_t>(row0 + t) * p.m_out + f0 + 8 * piece) = v;
+            }
+        }
+        __syncwarp();
+    }
+};
+
 // Waits as a whole warp: one poll and a vote when the phase is complete, the
 // bounded wait otherwise. False, for every lane, once the wait gave up.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int *err,
@@ -92,6 +204,28 @@ __device__ __forceinline__ void umma_i8_stage_pair(uint32_t d, uint32_t a, uint3
         "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%5], %7;\n\t}\n" ::"r"(d),
         "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(smem_u32(bar)), "r"(kDescHigh), "h"(static_cast<uint16_t>(0x3))
         : "memory");
+}
+
+// The same for one CTA; without the commit while another operand A of the stage
+// follows.
+template <bool COMMIT>
+__device__ __forceinline__ void umma_i8_stage(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate,
+                                              uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred e, p, t;\n\t.reg .b32 a1, a2, a3, b1, b2, b3;\n\t.reg .b64 x0, x1, x2, x3, y0, y1, y2, y3;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "add.u32 a1, %1, 2;\n\tadd.u32 a2, %1, 4;\n\tadd.u32 a3, %1, 6;\n\t"
+        "add.u32 b1, %2, 2;\n\tadd.u32 b2, %2, 4;\n\tadd.u32 b3, %2, 6;\n\t"
+        "mov.b64 x0, {%1, %5};\n\tmov.b64 x1, {a1, %5};\n\tmov.b64 x2, {a2, %5};\n\tmov.b64 x3, {a3, %5};\n\t"
+        "mov.b64 y0, {%2, %5};\n\tmov.b64 y1, {b1, %5};\n\tmov.b64 y2, {b2, %5};\n\tmov.b64 y3, {b3, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::i8 [%0], x0, y0, %3, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::i8 [%0], x1, y1, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::i8 [%0], x2, y2, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::i8 [%0], x3, y3, %3, t;\n\t}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHigh)
+        : "memory");
+    if (COMMIT && elect_one()) umma_commit(bar);
 }
 
 }  // namespace gemm

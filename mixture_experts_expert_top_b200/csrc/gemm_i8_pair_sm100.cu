@@ -45,47 +45,12 @@ constexpr int kScaleBytes = kEpiWarps * (kTokBlock / 2) * 4;     // token scales
 template <bool SWIGLU, int STAGES>
 struct I8PairCfg {
     static constexpr int kThreads = 64 + 32 * kEpiWarps;
-    // one warp's staging of 32 token rows: 16 or 32 features and 16 bytes that
-    // keep the eight rows of a stmatrix on different banks
-    static constexpr int kRowBytes = SWIGLU ? 48 : 80;
-    static constexpr int kOutBytes = kEpiWarps * 32 * kRowBytes;
+    static constexpr int kOutBytes = kEpiWarps * I8RowWriter<SWIGLU>::kBytes;
     static constexpr int kRingBytes = STAGES * kStage;
     static constexpr int kNumBars = 2 * STAGES + 2 + 2 + 1;
     static constexpr int kSmemBytes =
         1024 + kRingBytes + kOutBytes + kScaleBytes + 8 * kNumBars + 64 + 2 * (kMaxExperts + 1) * 4;
     static_assert(kSmemBytes + 64 <= kSmemLimit, "shared memory");
-};
-
-// The tiles of this pair in order, for a converged warp: every 32 tiles each
-// lane decodes one of them (a search over the experts and two divisions, about
-// 800 cycles), and each tile is then a few shuffles.
-struct TileFeed {
-    const int *pre, *off;
-    int E, MB, tile, step, total, left;
-    TileInfo mine;
-
-    __device__ __forceinline__ TileFeed(const int *pre_, const int *off_, int E_, int MB_, int first, int step_)
-        : pre(pre_), off(off_), E(E_), MB(MB_), tile(first), step(step_), total(pre_[E_]), left(0) {}
-
-    // False when there is none left.
-    __device__ __forceinline__ bool next(TileInfo &t) {
-        if (tile >= total) return false;
-        if (left == 0) {
-            const int lane = threadIdx.x & 31;
-            const long long at = tile + static_cast<long long>(lane) * step;
-            mine = decode_tile(at < total ? static_cast<int>(at) : tile, pre, off, E, MB, kTokBlock);
-            left = 32;
-        }
-        const int src = 32 - left;
-        t.e = __shfl_sync(0xffffffffu, mine.e, src);
-        t.mb = __shfl_sync(0xffffffffu, mine.mb, src);
-        t.row0 = __shfl_sync(0xffffffffu, mine.row0, src);
-        t.valid = __shfl_sync(0xffffffffu, mine.valid, src);
-        t.n_mma = (t.valid + 31) & ~31;              // kind::i8 across a pair takes N in steps of 32
-        --left;
-        tile += step;
-        return true;
-    }
 };
 
 template <bool SWIGLU, int STAGES>
@@ -146,7 +111,7 @@ grouped_gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __gri
     cluster_sync();                                          // barriers of both CTAs initialised
     tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_holder;
-    TileFeed feed(pre_s, off_s, E, MB, static_cast<int>(cluster_id_x()), static_cast<int>(cluster_count_x()));
+    TileFeed<kTokBlock, 32> feed(pre_s, off_s, E, MB, static_cast<int>(cluster_id_x()), static_cast<int>(cluster_count_x()));
     TileInfo ti;
 
     if (warp == 0) {
@@ -209,16 +174,10 @@ grouped_gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __gri
         // ====================== warps 2-9: epilogue (both CTAs) =================
         const int q = warp & 3;                              // TMEM lane quarter of this warp
         const int h = (warp - 2) >> 2;                       // column half: warps 2-5 first, 6-9 second
-        constexpr int kFeat = SWIGLU ? 16 : 32;              // features of a warp
-        constexpr int kPieces = kFeat / 8;                   // 16-byte pieces of its token rows
         const uint32_t tempty_leader0 = cluster_map(smem_u32(&tempty_bar[0]), 0);
         const uint32_t tempty_leader1 = cluster_map(smem_u32(&tempty_bar[1]), 0);
-        uint8_t *rows_s = out_s + (warp - 2) * 32 * C::kRowBytes;
+        const I8RowWriter<SWIGLU> writer(out_s + (warp - 2) * I8RowWriter<SWIGLU>::kBytes);
         float *sx_s = scale_s + (warp - 2) * (kTokBlock / 2);
-        // this lane's row address of a stmatrix: matrix lane / 8 is 8 features (down) or,
-        // gate/up, 8 features of token group lane / 16
-        const uint32_t st_addr = smem_u32(rows_s) + (SWIGLU ? ((lane >> 4) * 8 + (lane & 7)) * C::kRowBytes + ((lane >> 3) & 1) * 16
-                                                            : (lane & 7) * C::kRowBytes + (lane >> 3) * 16);
         int buf = 0;
         uint32_t bphase = 0;
         // TMEM accumulator buffer handed back to the MMA issuer once this
@@ -236,15 +195,8 @@ grouped_gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __gri
             const int split = (nch + 1) >> 1;
             const int c_lo = h ? split : 0, c_hi = h ? nch : split;
             const int f0 = SWIGLU ? ti.mb * 128 + 64 * rank + 16 * q : ti.mb * 256 + 128 * rank + 32 * q;
-            // weight scales of this thread's accumulator rows lane / 4 + 8 i (gate/up:
-            // i = 0, 1 gate, 2, 3 the matching up rows)
             float sw[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int f = f0 + (lane >> 2) + 8 * (SWIGLU ? i & 1 : i);
-                const size_t row = static_cast<size_t>(ti.e) * p.w_rows + f + (SWIGLU && i >= 2 ? p.m_out : 0);
-                sw[i] = f < p.m_out ? __ldg(ip.w_sf + row) : 0.f;
-            }
+            i8_weight_scales<SWIGLU>(ip, ti.e, f0, sw);
             // token scales of this half, kept in shared memory for the tile
             for (int c = c_lo; c < c_hi; ++c) {
                 const int n = 32 * c + lane;
@@ -264,41 +216,7 @@ grouped_gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __gri
                 tmem_ld_16x256b_x4(tb + (16u << 16) + 32 * c, b);
             };
             auto chunk = [&](const uint32_t (&a)[16], const uint32_t (&b)[16], int c) {
-                const float *sx = sx_s + 32 * (c - c_lo) + 2 * (lane & 3);
-                uint32_t lo[4], hi[4];                       // gate/up: features 0-7, 8-15 of each token group
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const float2 s = *reinterpret_cast<const float2 *>(sx + 8 * g);
-                    float v[8];                              // [row lane / 4 + 8 i][token 0, 1]
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t *r = i < 2 ? a + 4 * g + 2 * i : b + 4 * g + 2 * (i - 2);
-                        v[2 * i] = i8_scaled(r[0], sw[i], s.x);
-                        v[2 * i + 1] = i8_scaled(r[1], sw[i], s.y);
-                    }
-                    if constexpr (SWIGLU) {
-                        lo[g] = i8_bf16x2(i8_act(v[0], v[4]), i8_act(v[1], v[5]));
-                        hi[g] = i8_bf16x2(i8_act(v[2], v[6]), i8_act(v[3], v[7]));
-                        if (g & 1)
-                            stmatrix_x4_trans(st_addr + 8 * (g - 1) * C::kRowBytes, lo[g - 1], hi[g - 1], lo[g], hi[g]);
-                    } else {
-                        stmatrix_x4_trans(st_addr + 8 * g * C::kRowBytes, i8_bf16x2(v[0], v[1]), i8_bf16x2(v[2], v[3]),
-                                          i8_bf16x2(v[4], v[5]), i8_bf16x2(v[6], v[7]));
-                    }
-                }
-                __syncwarp();
-                const int piece = lane % kPieces;
-                if (f0 + 8 * piece < p.m_out) {
-#pragma unroll
-                    for (int i = 0; i < kPieces; ++i) {
-                        const int t = lane / kPieces + i * (32 / kPieces);
-                        const uint4 v = *reinterpret_cast<const uint4 *>(rows_s + t * C::kRowBytes + 16 * piece);
-                        if (32 * c + t < ti.valid)
-                            *reinterpret_cast<uint4 *>(p.out + static_cast<size_t>(ti.row0 + 32 * c + t) * p.m_out + f0 +
-                                                       8 * piece) = v;
-                    }
-                }
-                __syncwarp();
+                writer.write(p, a, b, sw, sx_s + 32 * (c - c_lo), f0, ti.row0 + 32 * c, ti.valid - 32 * c);
             };
             // two register sets: the next 32 columns load while this set is stored
             uint32_t a0[16], b0[16], a1[16], b1[16];

@@ -154,8 +154,9 @@ struct I8GemmArgs {
     const float *x_sf;          // [rows of base.a] token-row scales
 };
 cudaError_t launch_grouped_gemm_i8(const I8GemmArgs &g, cudaStream_t s);
-// ---- gemm_i8_rows_sm100.cu: the same for a few rows in all, without tensor cores
-cudaError_t launch_grouped_gemm_i8_rows(const I8GemmArgs &g, cudaStream_t s);
+// ---- gemm_i8_warp_sm100.cu: the same for few rows per expert, warp-level MMAs
+// fed straight from global memory
+cudaError_t launch_grouped_gemm_i8_warp(const I8GemmArgs &g, cudaStream_t s);
 // ---- gemm_i8_pair_sm100.cu: the same for many tokens per expert (permuted
 // rows, no perm), weights on M across a CTA pair
 cudaError_t launch_grouped_gemm_i8_pair(const I8GemmArgs &g, cudaStream_t s);
