@@ -102,14 +102,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volati
     return true;
 }
 
-// True in one lane of a converged warp, the same one every time.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}\n" : "=r"(r)::"memory");
-    return r != 0;
-}
-
 // ------------------------------------------------------ clusters (CTA pairs) --
 
 __device__ __forceinline__ uint32_t cluster_ctarank() {
@@ -203,27 +195,6 @@ __device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *m
         "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
         ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster_addr), "r"(x), "r"(y), "l"(policy)
-        : "memory");
-}
-
-// The same for a 5-D tensor (coordinates innermost first).
-__device__ __forceinline__ void tma_load_5d_pair(void *dst, const CUtensorMap *map, uint32_t bar_cluster_addr, int x,
-                                                 int c1, int c2, int c3, int c4, uint64_t policy) {
-    asm volatile(
-        "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        ".L2::cache_hint [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster_addr), "r"(x), "r"(c1), "r"(c2), "r"(c3), "r"(c4),
-        "l"(policy)
-        : "memory");
-}
-
-// 5-D tiled load by one CTA (coordinates innermost first).
-__device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int c1, int c2,
-                                            int c3, int c4, uint64_t policy) {
-    asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "l"(policy)
         : "memory");
 }
 
@@ -386,29 +357,6 @@ __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&r)
         : "memory");
 }
 
-// 16 lanes x 32 consecutive 32-bit TMEM columns -> 16 registers per thread, in
-// the layout of an MMA fragment: thread i holds, for each group g of 8
-// columns, columns 8g + 2(i%4) + {0, 1} of lane i/4 in registers 4g, 4g+1 and
-// of lane i/4 + 8 in registers 4g+2, 4g+3.
-__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
-}
-
-// Four 8x8 matrices of 16-bit elements in fragment layout (thread i: row i/4,
-// columns 2(i%4) + {0, 1}) to shared memory, transposed: the 16 bytes at the
-// address that lane 8m + c gives receive column c of matrix m.
-__device__ __forceinline__ void stmatrix_x4_trans(uint32_t smem_addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(smem_addr), "r"(a),
-                 "r"(b), "r"(c), "r"(d)
-                 : "memory");
-}
-
 __device__ __forceinline__ void tmem_wait_ld() {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
@@ -488,19 +436,6 @@ __device__ __forceinline__ void umma_mxf8_ss(uint32_t d_tmem, uint64_t a_desc, u
         "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
         : "memory");
-}
-
-// --- int8 operands, int32 accumulator (kind::i8) -------------------------------
-
-// Instruction descriptor, kind::i8: signed 8-bit A and B (both K-major), int32
-// D, shape M x N (M = 128: N = 16 or a multiple of 16 in [32, 256]; M = 256
-// across a CTA pair: a multiple of 32 in [32, 256]).
-__host__ __device__ __forceinline__ uint32_t idesc_i8_i32(int M, int N) {
-    return (2u << 4)                                        // D format: s32
-           | (1u << 7)                                      // A format: s8
-           | (1u << 10)                                     // B format: s8
-           | (static_cast<uint32_t>(N >> 3) << 17)          // N >> 3
-           | (static_cast<uint32_t>(M >> 4) << 24);         // M >> 4
 }
 
 // ----------------------------------------------------------------- numerics --

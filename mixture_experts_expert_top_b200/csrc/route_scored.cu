@@ -267,7 +267,7 @@ __device__ __noinline__ int refine_64(const RouterArgs &a, const L *row, float m
         const float x = clean_logit(load_logit(row + id));
         double s;
         if (soft)
-            s = (x == m ? 1.0 : exp(static_cast<double>(x) - m)) / sum;
+            s = m == -INFINITY ? 0.0 : (x == m ? 1.0 : exp(static_cast<double>(x) - m)) / sum;
         else
             s = 1.0 / (1.0 + exp(-static_cast<double>(x)));
         key = choice_key(s + static_cast<double>(a.bias[id]));

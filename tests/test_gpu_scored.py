@@ -172,6 +172,23 @@ def test_special_biases(score):
     check(l, torch.where(torch.arange(E) < 8, 3e38, -3e38), 8, score=score)
 
 
+def test_near_biases_decide_rows_without_scores():
+    # every logit -inf: all scores are 0 and the order is the biases', which here
+    # differ by one fp32 step near 1e-30 and would vanish beside any score
+    E = 16
+    b = torch.full((E,), -1.0) * 1e-28
+    b[3] = 1e-30
+    b[7] = torch.nextafter(b[3], torch.tensor(1.0))
+    b[11] = torch.nextafter(b[7], torch.tensor(1.0))
+    l = torch.full((3, E), -INF)
+    l[1] = NAN
+    for score in ("softmax", "sigmoid"):
+        ids, w = run(l, b, 3, score=score)
+        assert np.array_equal(ids, np.tile([11, 7, 3], (3, 1))) and np.all(w == 0)
+        check(l, b, 3, score=score)
+        check(l, b, 3, score=score, n_group=4, topk_group=3, group_top=2)
+
+
 def test_equals_moe_route_where_both_apply():
     l = logits_of(300, 128, 8).to(DEV)
     sh = moe.Shape.of(300, 128, 64, 128, 8)
