@@ -240,6 +240,98 @@ def test_prefill_sized_products():
     check(case(2048, 2048, 768, 16, 8, skew=1.0), gather_too=False)
 
 
+def test_arrays_past_32_bit_offsets():
+    # more than 2^31 elements in the quantised rows, in gate/up's token rows and in
+    # down's output; the last rows are checked
+    rows, K = 66000, 32768
+    tail = 40
+    x = torch.zeros(rows, K, dtype=torch.bfloat16, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x[-tail:] = torch.randn(tail, K, generator=g, device=DEV).to(torch.bfloat16)
+    q, s = torch.empty(rows, K, dtype=torch.int8, device=DEV), torch.empty(rows, device=DEV)
+    moe.moe_i8_quantize(x, rows, K, q, s)
+    rq, rs = _plain.int8_rows(x[-tail:])
+    assert torch.equal(q[-tail:], rq) and torch.equal(s[-tail:], rs) and bool((s[:-tail] == 0).all())
+    del x
+    off = torch.tensor([0, rows - 10, rows], dtype=torch.int32, device=DEV)
+    # gate/up: H = 32768, I = 16; down: H = 32768, I = 16
+    sh = moe.Shape.of(rows, K, 16, 2, 1, "int8")
+    w_gu, gs = codes(g, 2, 32, K), scales(g, 2, 32) * 1e-6
+    act = torch.empty(rows, 16, dtype=torch.bfloat16, device=DEV)
+    moe.moe_grouped_gemm_swiglu_i8(q, s, None, off, w_gu, gs, sh, act)
+    v = _plain.grouped_int8(q[-tail:], s[-tail:], None, (off - (rows - tail)).clamp_min(0), w_gu, gs, 1)
+    close_act(act[-tail:], v)
+    del q
+    aq, as_ = codes(g, rows, 16), scales(g, rows)
+    w_d, ds = codes(g, 2, K, 16), scales(g, 2, K)
+    y = torch.empty(rows, K, dtype=torch.bfloat16, device=DEV)
+    moe.moe_grouped_gemm_down_i8(aq, as_, off, w_d, ds, sh, y)
+    close_y(y[-tail:], _plain.grouped_int8(aq[-tail:], as_[-tail:], None, (off - (rows - tail)).clamp_min(0), w_d, ds, 1))
+
+
+def test_first_call_of_every_kernel_may_be_captured():
+    # a fresh process whose first calls are under capture: set-up calls (function
+    # attributes, occupancy, tensor maps) are legal there
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch, mixture_experts_expert_top_b200 as moe
+D = dict(device="cuda")
+T, H, I, E, k = 40, 256, 128, 8, 2
+x = torch.randn(T, H, **D).to(torch.bfloat16); l = torch.randn(T, E, **D); b = torch.zeros(E, **D)
+w = torch.ones(H, dtype=torch.bfloat16, **D)
+q, s = torch.empty(T, H, dtype=torch.int8, **D), torch.empty(T, **D)
+wg = torch.randint(-9, 9, (E, 2 * I, H), dtype=torch.int8, **D); wd = torch.randint(-9, 9, (E, H, I), dtype=torch.int8, **D)
+gs, ds = torch.rand(E, 2 * I, **D), torch.rand(E, H, **D)
+outs = []
+sh = moe.Shape.of(T, H, I, E, k, "int8")
+ws = torch.empty(moe.moe_workspace_size(sh), dtype=torch.uint8, **D)
+out, out2 = torch.empty_like(x), torch.empty_like(x)
+r = moe.Router.of("sigmoid")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    moe.moe_rmsnorm(x, None, w, 1e-6, T, H, moe.FMT_INT8, None, None, q, s)
+    moe.moe_forward_scored(x, l, b, r, wg, gs, wd, ds, sh, out, ws)
+g.replay(); torch.cuda.synchronize()
+moe.moe_forward_scored(x, l, b, r, wg, gs, wd, ds, sh, out2, ws)
+torch.cuda.synchronize()
+assert torch.equal(out.view(torch.int16), out2.view(torch.int16)) and moe.moe_get_device_error() == 0
+print("captured ok")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=240)
+    assert r.returncode == 0 and "captured ok" in r.stdout, r.stderr[-2000:]
+
+
+def test_two_calls_at_once_on_two_streams():
+    c = case(900, 512, 256, 8, 2)
+    d = case(60, 512, 256, 8, 2, seed=3)
+    refs = [down(c), gate_up(c, c["hq"], c["hs"], c["perm"]), down(d), gate_up(d, d["hq"], d["hs"], d["perm"])]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[torch.empty_like(r) for r in refs] for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for st, o in zip(streams, outs):
+            moe.moe_grouped_gemm_down_i8(c["aq"], c["as"], c["off"], c["w_d"], c["ds"], c["shape"], o[0], st)
+            moe.moe_grouped_gemm_swiglu_i8(c["hq"], c["hs"], c["perm"], c["off"], c["w_gu"], c["gs"], c["shape"], o[1], st)
+            moe.moe_grouped_gemm_down_i8(d["aq"], d["as"], d["off"], d["w_d"], d["ds"], d["shape"], o[2], st)
+            moe.moe_grouped_gemm_swiglu_i8(d["hq"], d["hs"], d["perm"], d["off"], d["w_gu"], d["gs"], d["shape"], o[3], st)
+    torch.cuda.synchronize()
+    for o in outs:
+        for a, b in zip(o, refs):
+            assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+# rows per expert around the sizes where another kernel or tile takes over (16 rows
+# on average and 64 tokens, 24, 48; N steps of 16 and 32, blocks of 32, 64, 128, 256)
+@pytest.mark.parametrize("T", [8, 9, 16, 17, 31, 32, 33, 48, 49, 63, 64, 65, 96, 97, 127, 128, 160, 256, 511, 513])
+def test_kernel_boundaries(T):
+    check(case(T, 272, 144, 4, 2, seed=T))
+    check(case(T, 144, 80, 1, 1, seed=T))
+
+
 # ---- the layer ----------------------------------------------------------------
 
 def layer_inputs(T, H, I, E, k, seed=0, n_shared=0):

@@ -220,6 +220,19 @@ def test_large_batch_on_a_side_stream():
     assert np.all(np.abs(w - rw) <= 2.0 ** -24 * 60 * rw)
 
 
+def test_logits_past_32_bit_offsets():
+    T, E, k = 2_200_000, 1000, 2
+    l = torch.zeros(T, E, dtype=torch.bfloat16, device=DEV)
+    tail = logits_of(50, E, 6, torch.bfloat16)
+    l[-50:] = tail.to(DEV)
+    b = bias_of(E, 6).to(DEV)
+    ids, w = torch.empty(T, k, dtype=torch.int32, device=DEV), torch.empty(T, k, device=DEV)
+    moe.moe_route_scored(l, b, moe.Router.of("sigmoid", logits="bf16"), moe.Shape.of(T, 8, 8, E, k), ids, w)
+    torch.cuda.synchronize()
+    assert np.array_equal(ids[-50:].cpu().numpy(), _plain.route_scored(tail, b.cpu(), k, "sigmoid")[0])
+    assert bool((ids[:-50] == torch.sort(b, descending=True, stable=True).indices[:k].to(torch.int32)).all())
+
+
 def test_captured_and_replayed_on_new_logits():
     T, E, k = 64, 64, 6
     sh, r = moe.Shape.of(T, 128, 64, E, k), moe.Router.of("sigmoid", 8, 3, 2)
