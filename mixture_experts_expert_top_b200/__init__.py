@@ -213,22 +213,47 @@ def _p(t, *dtypes) -> Optional[int]:
     return t.data_ptr()
 
 
-def _pd(t, n: int, dtype, dev: int) -> Optional[int]:
-    """_p of a contiguous tensor of this dtype with at least n elements on CUDA
-    device dev (None for None): a host tensor, a tensor of another device or a
-    short one is refused before the library is called. An address (int) passes
-    as it is."""
-    if t is None or t.__class__ is int:
-        return t
-    if t.dtype is dtype and t.numel() >= n and t.get_device() == dev and t.is_contiguous():
-        return t.data_ptr()
-    if t.dtype is not dtype:
-        raise TypeError(f"libmoe_b200: expected a tensor of {dtype}, got {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError("tensors passed to libmoe_b200 must be contiguous")
-    if t.numel() < n:
-        raise ValueError(f"libmoe_b200: expected at least {n} elements, got a tensor of shape {tuple(t.shape)}")
-    raise ValueError(f"libmoe_b200: expected a tensor on the current CUDA device, got one on {t.device}")
+# element types as marshal.cpp has them (c10::ScalarType codes)
+_U8, _I8, _I32, _F32, _BF16 = 0, 1, 3, 6, 15
+_DTYPES = {_U8: U8, _I8: I8, _I32: I32, _F32: F32, _BF16: BF16}
+
+
+def _addresses(dev: int, *spec):
+    """Addresses of tensors given as (tensor, elements, type code) triples: each
+    contiguous, of that type, with at least that many elements, on CUDA device
+    dev; anything else (a host tensor, one of another device, a short one) is
+    refused before the library is called. None and addresses (int) pass as they
+    are. The checks run in _marshal; this function loads it and, on a refusal,
+    says what is wrong."""
+    global _checked
+    if _checked is _addresses:
+        from . import build as _build
+        if not _build.marshal_up_to_date():
+            try:
+                _build.build_marshal()
+            except Exception as e:      # noqa: BLE001 - re-raised with the path
+                raise RuntimeError(f"{_build.MARSHAL} is missing or older than its source and could not be "
+                                   f"built ({e}): build it with `python -m mixture_experts_expert_top_b200.build`")
+        from . import _marshal
+        _checked = _marshal.addresses
+    found = _checked(dev, *spec)
+    if found is not None:
+        return found
+    given = [x for x in zip(spec[::3], spec[1::3], spec[2::3]) if x[0] is not None and x[0].__class__ is not int]
+    for t, n, code in given:
+        if not isinstance(t, torch.Tensor) or t.dtype is not _DTYPES[code]:
+            raise TypeError(f"libmoe_b200: expected a tensor of {_DTYPES[code]}, got {getattr(t, 'dtype', type(t))}")
+    for t, n, code in given:
+        if t.layout is not torch.strided or not t.is_contiguous():
+            raise ValueError("tensors passed to libmoe_b200 must be contiguous")
+        if t.numel() < n:
+            raise ValueError(f"libmoe_b200: expected at least {n} elements, got a tensor of shape {tuple(t.shape)}")
+        if t.get_device() != dev:
+            raise ValueError(f"libmoe_b200: expected a tensor on the current CUDA device, got one on {t.device}")
+    raise RuntimeError("libmoe_b200: a tensor was refused")
+
+
+_checked = _addresses          # _marshal.addresses from the first call on
 
 
 _cuda_used = False
@@ -296,21 +321,19 @@ def moe_route_scored(logits, bias, router: Router, shape, topk_ids, topk_w, stre
     sh, d = _shape(shape), _dev()
     T, _, _, E, k, _, S = _dims(sh)
     n = T * (k + S)
-    _check(lib().moe_route_scored(_pd(logits, T * E, BF16 if router.logits else F32, d), _pd(bias, E, F32, d),
-                                  router, sh, _pd(topk_ids, n, I32, d), _pd(topk_w, n, F32, d), _s(stream, d)),
-           "moe_route_scored")
+    spec = (logits, T * E, _BF16 if router.logits else _F32, bias, E, _F32, topk_ids, n, _I32, topk_w, n, _F32)
+    lg, b, ids, w = _checked(d, *spec) or _addresses(d, *spec)
+    _check(lib().moe_route_scored(lg, b, router, sh, ids, w, _s(stream, d)), "moe_route_scored")
 
 
 def moe_rmsnorm(x, residual, weight, eps: float, rows: int, H: int, fmt, residual_out, y, q=None, scales=None,
                 stream=None) -> None:
     n, d = rows * H, _dev()
-    if fmt == FMT_INT8:
-        q_p, s_p = _pd(q, n, I8, d), _pd(scales, rows, F32, d)
-    else:
-        q_p, s_p = _pd(q, n, U8, d), _pd(scales, n // 32, U8, d)
-    _check(lib().moe_rmsnorm(_pd(x, n, BF16, d), _pd(residual, n, BF16, d), _pd(weight, H, BF16, d), eps, rows, H, fmt,
-                             _pd(residual_out, n, BF16, d), _pd(y, n, BF16, d), q_p, s_p, _s(stream, d)),
-           "moe_rmsnorm")
+    q_type, s_type, n_scales = (_I8, _F32, rows) if fmt == FMT_INT8 else (_U8, _U8, n // 32)
+    spec = (x, n, _BF16, residual, n, _BF16, weight, H, _BF16, residual_out, n, _BF16, y, n, _BF16, q, n, q_type,
+            scales, n_scales, s_type)
+    px, pr, pw, po, py, pq, ps = _checked(d, *spec) or _addresses(d, *spec)
+    _check(lib().moe_rmsnorm(px, pr, pw, eps, rows, H, fmt, po, py, pq, ps, _s(stream, d)), "moe_rmsnorm")
 
 
 def moe_permute(topk_ids, shape, counts, offsets, perm, inv_perm, hidden=None, hidden_perm=None,
@@ -397,9 +420,9 @@ def moe_grouped_gemm_down_mx(act_q, act_scales, offsets, w_d, w_d_scales, shape,
 
 def moe_i8_quantize(x, rows: int, K: int, q, scales, stream=None) -> None:
     n, d = rows * K, _dev()
-    _check(lib().moe_i8_quantize(_pd(x, n, BF16, d), rows, K, _pd(q, n, I8, d), _pd(scales, rows, F32, d),
-                                 _s(stream, d)),
-           "moe_i8_quantize")
+    spec = (x, n, _BF16, q, n, _I8, scales, rows, _F32)
+    px, pq, ps = _checked(d, *spec) or _addresses(d, *spec)
+    _check(lib().moe_i8_quantize(px, rows, K, pq, ps, _s(stream, d)), "moe_i8_quantize")
 
 
 def moe_grouped_gemm_swiglu_i8(a_q, a_scales, perm, offsets, w_gu, w_gu_scales, shape, act, stream=None) -> None:
@@ -407,42 +430,41 @@ def moe_grouped_gemm_swiglu_i8(a_q, a_scales, perm, offsets, w_gu, w_gu_scales, 
     T, H, I, E, k, _, S = _dims(sh)
     P, E = T * (k + S), E + S
     rows = P if perm is None else T
-    _check(lib().moe_grouped_gemm_swiglu_i8(_pd(a_q, rows * H, I8, d), _pd(a_scales, rows, F32, d),
-                                            _pd(perm, P, I32, d), _pd(offsets, E + 1, I32, d),
-                                            _pd(w_gu, E * 2 * I * H, I8, d), _pd(w_gu_scales, E * 2 * I, F32, d), sh,
-                                            _pd(act, P * I, BF16, d), _s(stream, d)),
-           "moe_grouped_gemm_swiglu_i8")
+    spec = (a_q, rows * H, _I8, a_scales, rows, _F32, perm, P, _I32, offsets, E + 1, _I32, w_gu, E * 2 * I * H, _I8,
+            w_gu_scales, E * 2 * I, _F32, act, P * I, _BF16)
+    pa, ps, pp, po, pw, pg, pc = _checked(d, *spec) or _addresses(d, *spec)
+    _check(lib().moe_grouped_gemm_swiglu_i8(pa, ps, pp, po, pw, pg, sh, pc, _s(stream, d)), "moe_grouped_gemm_swiglu_i8")
 
 
 def moe_grouped_gemm_down_i8(act_q, act_scales, offsets, w_d, w_d_scales, shape, y, stream=None) -> None:
     sh, d = _shape(shape), _dev()
     T, H, I, E, k, _, S = _dims(sh)
     P, E = T * (k + S), E + S
-    _check(lib().moe_grouped_gemm_down_i8(_pd(act_q, P * I, I8, d), _pd(act_scales, P, F32, d),
-                                          _pd(offsets, E + 1, I32, d), _pd(w_d, E * H * I, I8, d),
-                                          _pd(w_d_scales, E * H, F32, d), sh, _pd(y, P * H, BF16, d), _s(stream, d)),
-           "moe_grouped_gemm_down_i8")
+    spec = (act_q, P * I, _I8, act_scales, P, _F32, offsets, E + 1, _I32, w_d, E * H * I, _I8, w_d_scales, E * H, _F32,
+            y, P * H, _BF16)
+    pa, ps, po, pw, pg, py = _checked(d, *spec) or _addresses(d, *spec)
+    _check(lib().moe_grouped_gemm_down_i8(pa, ps, po, pw, pg, sh, py, _s(stream, d)), "moe_grouped_gemm_down_i8")
 
 
 def moe_forward_scored(hidden, logits, bias, router: Router, w_gu, w_gu_scales, w_d, w_d_scales, shape, out, ws,
                        stream=None) -> None:
     sh, d = _shape(shape), _dev()
-    T, H, I, E = sh.T, sh.H, sh.I, sh.experts
+    T, H, I, E, _, fmt, S = _dims(sh)
+    Et = E + S
     # per weight row of K elements: codes and scales, and their types
-    row = {FMT_BF16: (lambda K: K, lambda K: 0, BF16, BF16),
-           FMT_INT4_G128: (lambda K: K // 2, lambda K: K // 128, U8, BF16),
-           FMT_MXFP8: (lambda K: K, lambda K: K // 32, U8, U8),
-           FMT_MXFP4: (lambda K: K // 2, lambda K: K // 32, U8, U8),
-           FMT_INT8: (lambda K: K, lambda K: 1, I8, F32)}
-    if sh.fmt not in row:
+    row = {FMT_BF16: (lambda K: K, lambda K: 0, _BF16, _BF16),
+           FMT_INT4_G128: (lambda K: K // 2, lambda K: K // 128, _U8, _BF16),
+           FMT_MXFP8: (lambda K: K, lambda K: K // 32, _U8, _U8),
+           FMT_MXFP4: (lambda K: K // 2, lambda K: K // 32, _U8, _U8),
+           FMT_INT8: (lambda K: K, lambda K: 1, _I8, _F32)}
+    if fmt not in row:
         raise MoeError(1, "moe_forward_scored")
-    codes, scales, w_dt, s_dt = row[sh.fmt]
-    nbytes = ws.numel() * ws.element_size()
-    _check(lib().moe_forward_scored(_pd(hidden, T * H, BF16, d), _pd(logits, T * sh.E, BF16 if router.logits else F32, d),
-                                    _pd(bias, sh.E, F32, d), router, _pd(w_gu, E * 2 * I * codes(H), w_dt, d),
-                                    _pd(w_gu_scales, E * 2 * I * scales(H), s_dt, d),
-                                    _pd(w_d, E * H * codes(I), w_dt, d), _pd(w_d_scales, E * H * scales(I), s_dt, d),
-                                    sh, _pd(out, T * H, BF16, d), _pd(ws, 0, ws.dtype, d), nbytes, _s(stream, d)),
+    codes, scales, w_type, s_type = row[fmt]
+    spec = (hidden, T * H, _BF16, logits, T * E, _BF16 if router.logits else _F32, bias, E, _F32,
+            w_gu, Et * 2 * I * codes(H), w_type, w_gu_scales, Et * 2 * I * scales(H), s_type,
+            w_d, Et * H * codes(I), w_type, w_d_scales, Et * H * scales(I), s_type, out, T * H, _BF16, ws, 0, _U8)
+    ph, pl, pb, pg, pgs, pd, pds, po, pws = _checked(d, *spec) or _addresses(d, *spec)
+    _check(lib().moe_forward_scored(ph, pl, pb, router, pg, pgs, pd, pds, sh, po, pws, ws.numel(), _s(stream, d)),
            "moe_forward_scored")
 
 

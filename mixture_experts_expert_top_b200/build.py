@@ -1,4 +1,5 @@
-"""Build libmoe_b200.so (CUDA C++ for sm_100a) in-tree with nvcc.
+"""Build libmoe_b200.so (CUDA C++ for sm_100a) in-tree with nvcc, and the
+binding's tensor checks (_marshal.so, C++ against Python and torch) with g++.
 
 The library is plain CUDA: no torch headers, no Python symbols. It links the
 CUDA runtime statically and reaches the driver's cuTensorMapEncodeTiled
@@ -20,6 +21,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libmoe_b200.so")
 LIB_DEBUG = os.path.join(HERE, "libmoe_b200_debug.so")
+MARSHAL = os.path.join(HERE, "_marshal.so")
+MARSHAL_SOURCE = os.path.join(CSRC, "marshal.cpp")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 NVCC_FLAGS = [
@@ -56,12 +59,37 @@ def up_to_date(debug_bounds: bool = False) -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
+def marshal_up_to_date() -> bool:
+    return os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL_SOURCE) <= os.path.getmtime(MARSHAL)
+
+
+def build_marshal(force: bool = False, verbose: bool = False) -> str:
+    """Compiles csrc/marshal.cpp into _marshal.so (g++, torch's headers)."""
+    if not force and marshal_up_to_date():
+        return MARSHAL
+    import sysconfig
+
+    import torch
+    root = os.path.join(os.path.dirname(torch.__file__))
+    lib = os.path.join(root, "lib")
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(root, "include"), "-I", "/usr/local/cuda/include",
+           MARSHAL_SOURCE, "-o", MARSHAL + ".tmp", "-L", lib, f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    if verbose:
+        print(" ".join(cmd))
+    subprocess.run(cmd, check=True)
+    os.replace(MARSHAL + ".tmp", MARSHAL)
+    return MARSHAL
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False, debug_bounds: bool = False) -> str:
     """Compiles every csrc/*.cu for sm_100a and links the shared library.
     debug_bounds=True builds libmoe_b200_debug.so with -DMOE_DEBUG_BOUNDS
     (range checks on perm-derived row indices and on the expert offsets,
     raising device error 4) from the same sources."""
     lib = LIB_DEBUG if debug_bounds else LIB
+    build_marshal(force, verbose)
     if not force and up_to_date(debug_bounds):
         return lib
     build_dir = os.path.join(BUILD_DIR, "debug_bounds") if debug_bounds else BUILD_DIR
