@@ -101,10 +101,16 @@ __device__ __forceinline__ uint32_t i8_bf16x2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&b);
 }
 
-// silu(g) * u. The fast exponential and quotient are within 2^-20 (1 + |g|) of
-// silu's value, below the bf16 rounding's 2^-8; exp(-g) past the fp32 range
-// gives a quotient of 0.
-__device__ __forceinline__ float i8_act(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
+// silu(g) * u = g / (1 + exp(-g)) * u with the approximate exponential and
+// reciprocal (2^-22 and 2^-23, and 2^-23 |g| for the exponential's argument):
+// within 2^-20 (1 + |g|), below the bf16 rounding's 2^-8. exp(-g) past the fp32
+// range gives 0.
+__device__ __forceinline__ float i8_act(float g, float u) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.44269504f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return g * r * u;
+}
 
 // Tensor map of gate/up weights [E, 2I, K] int8 for tiles whose rows alternate
 // 16 gate rows and the 16 up rows of the same features: (K, 16, gate/up, I/16,

@@ -192,22 +192,38 @@ grouped_gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __gri
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster_relaxed(buf ? tempty_leader1 : tempty_leader0);
         };
-        while (feed.next(ti)) {
-            // this half's columns: chunks [c_lo, c_hi) of 32 tokens
+        // A tile's scales are loaded while the tile before it is stored: the weight
+        // rows' and, one per lane, the tokens' of this half, chunks [c_lo, c_hi) of 32.
+        float sw_next[4], sx_next[kTokBlock / 64];
+        auto fetch = [&]() {
+            const int nch = (ti.valid + 31) >> 5, split = (nch + 1) >> 1;
+            const int lo = h ? split : 0, hi = h ? nch : split;
+            i8_weight_scales<SWIGLU>(ip, ti.e, ti.mb * kFeatPerTile + (SWIGLU ? 64 * rank + 16 * q : 128 * rank + 32 * q),
+                                     sw_next);
+#pragma unroll
+            for (int c = 0; c < kTokBlock / 64; ++c) {
+                const int n = 32 * (lo + c) + lane;
+                sx_next[c] = lo + c < hi && n < ti.valid ? __ldg(ip.x_sf + ti.row0 + n) : 0.f;
+            }
+        };
+        bool more = feed.next(ti);
+        if (more) fetch();
+        while (more) {
             const int nch = (ti.valid + 31) >> 5;
             const int split = (nch + 1) >> 1;
             const int c_lo = h ? split : 0, c_hi = h ? nch : split;
-            const int f0 = SWIGLU ? ti.mb * 128 + 64 * rank + 16 * q : ti.mb * 256 + 128 * rank + 32 * q;
+            const int f0 = ti.mb * kFeatPerTile + (SWIGLU ? 64 * rank + 16 * q : 128 * rank + 32 * q);
+            const int row0 = ti.row0, valid = ti.valid;
             float sw[4];
-            i8_weight_scales<SWIGLU>(ip, ti.e, f0, sw);
-            // token scales of this half, kept in shared memory for the tile
-            for (int c = c_lo; c < c_hi; ++c) {
-                const int n = 32 * c + lane;
-                sx_s[n - 32 * c_lo] = n < ti.valid ? __ldg(ip.x_sf + ti.row0 + n) : 0.f;
-            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sw[i] = sw_next[i];
+#pragma unroll
+            for (int c = 0; c < kTokBlock / 64; ++c) sx_s[32 * c + lane] = sx_next[c];
             __syncwarp();
             if (!warp_wait(&tfull_bar[buf], bphase, abort_flag, p.err, 128)) break;
             tc_fence_after_sync();
+            more = feed.next(ti);
+            if (more) fetch();
             if (c_lo >= c_hi) {
                 release();
                 if (++buf == 2) { buf = 0; bphase ^= 1; }
@@ -219,7 +235,7 @@ grouped_gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __gri
                 tmem_ld_16x256b_x4(tb + (16u << 16) + 32 * c, b);
             };
             auto chunk = [&](const uint32_t (&a)[16], const uint32_t (&b)[16], int c) {
-                writer.write(p, a, b, sw, sx_s + 32 * (c - c_lo), f0, ti.row0 + 32 * c, ti.valid - 32 * c);
+                writer.write(p, a, b, sw, sx_s + 32 * (c - c_lo), f0, row0 + 32 * c, valid - 32 * c);
             };
             // two register sets: the next 32 columns load while this set is stored
             uint32_t a0[16], b0[16], a1[16], b1[16];
