@@ -202,3 +202,16 @@ def test_many_rows():
     x, r, w = inputs(20000, 128)
     check(x, r, w, "int8")
     check(x, r, w, "mxfp8")
+
+
+def test_a_lazily_shared_output_leaves_its_twin():
+    """An output that shares its storage copy-on-write gets its own before the
+    kernel writes: the tensor that it was cloned from keeps its values."""
+    x = torch.randn(4, 256, device=DEV).to(torch.bfloat16)
+    q0, s0 = torch.full((4, 256), 7, dtype=torch.int8, device=DEV), torch.full((4,), 3.0, device=DEV)
+    q, s = torch._lazy_clone(q0), torch._lazy_clone(s0)
+    moe.moe_i8_quantize(x, 4, 256, q, s)
+    want_q, want_s = torch.empty_like(q0), torch.empty_like(s0)
+    moe.moe_i8_quantize(x, 4, 256, want_q, want_s)
+    assert torch.equal(q, want_q) and torch.equal(s, want_s)
+    assert bool((q0 == 7).all()) and bool((s0 == 3.0).all())
