@@ -32,6 +32,10 @@ namespace moe {
 namespace {
 
 constexpr int kWarpsPerBlock = 4;
+// From this many rows on (20 warps on each of 148 SMs) one warp weighs several
+// rows: 16384 x 256 with groups 18.4 -> 16.2 us, 4096 x 128 4.1 -> 3.6 us. With
+// fewer the wait for the block's other warps shows (2048 x 128 3.3 -> 3.6 us).
+constexpr int kSharedWeighingRows = 20 * 148;
 
 struct RouterArgs {
     const void *logits;
@@ -582,24 +586,13 @@ __device__ __forceinline__ int select_choices(const RouterArgs &a, const L *row,
     return static_cast<int>(kIdMask - (my_key & kIdMask));
 }
 
-// 32 warps per SM up to 256 experts (64 registers): the row's work is a chain of
-// reductions, and other warps fill its latency (16384 x 256 with groups: 18.4
-// us; 75 registers 20.5 us, 48 registers 19.9).
+// The row's experts, that of slot j in lane j (j < k). x: the lane's logits; m:
+// softmax, the row's largest logit.
 template <int N, typename L>
-__global__ void __launch_bounds__(kWarpsPerBlock * 32, N <= 8 ? 8 : 1)
-route_scored_kernel(const __grid_constant__ RouterArgs a) {
-    extern __shared__ double by_all[];                           // [kWarpsPerBlock][E], only with groups
-    griddep_launch_dependents();
-    griddep_wait();
-    const int lane = threadIdx.x & 31;
-    const int warp = threadIdx.x >> 5;
-    const int t = blockIdx.x * kWarpsPerBlock + warp;
-    if (t >= a.T) return;
-    const L *row = static_cast<const L *>(a.logits) + static_cast<size_t>(t) * a.E;
-    const int e0 = lane * N;
+__device__ __forceinline__ int select_row(const RouterArgs &a, const L *row, double *by_s, float (&x)[N], float &m) {
+    const int e0 = (threadIdx.x & 31) * N;
     const bool soft = a.score == MOE_SCORE_SOFTMAX;
-    float x[N];
-    float m = -INFINITY;
+    m = -INFINITY;
     load_lane<N>(row, e0, a.E, a.vec, -INFINITY, x);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -607,7 +600,6 @@ route_scored_kernel(const __grid_constant__ RouterArgs a) {
         m = fmaxf(m, x[i]);
     }
     if (soft) m = warp_max(m);
-    double *by_s = by_all + static_cast<size_t>(warp) * a.E;
     const bool by_logit = a.bias == nullptr;
     int id;
     if (by_logit && a.n_group == 1) {
@@ -631,47 +623,113 @@ route_scored_kernel(const __grid_constant__ RouterArgs a) {
             if (count < 0) id = select_64<N, L>(a, row, m, bits);
         }
     }
-    // The weight of slot j, in lane j. Renormalised, only ratios of scores count:
-    // softmax takes them relative to the largest selected logit, and so does a
-    // sigmoid whose selected scores are all below e^-60 (there s = exp(l) to
-    // fp32), so no sum underflows.
+    return id;
+}
+
+// The sum of exp(l - m) over the row in x.
+template <int N>
+__device__ __forceinline__ float row_sum(const RouterArgs &a, const float (&x)[N], float m) {
+    const int e0 = (threadIdx.x & 31) * N;
+    float z = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (e0 + i < a.E) z += x[i] == m ? 1.0f : expf(x[i] - m);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    return z;
+}
+
+// The weight of slot j in lane j of the W that hold token t, and the row's
+// outputs. Renormalised, only ratios of scores count: softmax takes them
+// relative to the largest selected logit, and so does a sigmoid whose selected
+// scores are all below e^-60 (there s = exp(l) to fp32), so no sum underflows.
+template <int W, typename L, typename Sum>
+__device__ __forceinline__ void weigh_row(const RouterArgs &a, const L *row, int t, int id, float m, const Sum &sum_of) {
+    const int slot = W == 32 ? threadIdx.x & 31 : threadIdx.x % W;
+    const bool soft = a.score == MOE_SCORE_SOFTMAX;
+    const bool in = W == 32 || t < a.T;                          // a block's last rows may be behind T
+    const bool live = slot < a.k && in;
     float l = -INFINITY;
     bool off = false;
-    if (lane < a.k) {
+    if (live) {
         l = clean_logit(load_logit(row + id));
         off = a.bias && !(a.bias[id] > -INFINITY);
     }
-    const float lmax = warp_max(off ? -INFINITY : l);
+    float lmax = off ? -INFINITY : l;
+    if constexpr (W == 32) {
+        lmax = warp_max(lmax);
+    } else {
+#pragma unroll
+        for (int o = W / 2; o > 0; o >>= 1) lmax = fmaxf(lmax, __shfl_xor_sync(0xffffffffu, lmax, o));
+    }
     float s;
     if (soft && !a.renormalize) {
-        float z = 0.f;
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (e0 + i < a.E) z += x[i] == m ? 1.0f : expf(x[i] - m);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+        const float z = sum_of();
         s = (l == m ? 1.0f : expf(l - m)) / z;
     } else if (soft || (a.renormalize && lmax < -60.0f)) {
         s = l == lmax ? 1.0f : expf(l - lmax);
     } else {
         s = fast_rcp(1.0f + expf(-l));
     }
-    if (off || l == -INFINITY || lane >= a.k) s = 0.f;
+    if (off || l == -INFINITY || !live) s = 0.f;
     float wt = s;
     if (a.renormalize) {
         float sum = 0.f;                                             // slot order; lanes from k on add 0
         for (int j = 0; j < a.k; j += 8)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum += __shfl_sync(0xffffffffu, s, j + i);
+            for (int i = 0; i < 8; ++i) sum += __shfl_sync(0xffffffffu, s, j + i, W);
         wt = sum > 0.f ? __fdiv_rn(s, sum) : 0.f;
     }
     wt *= a.scale;
-    int out_id = id;
-    shared_slot(lane, a.k, a.E, out_id, wt);
+    shared_slot(slot, a.k, a.E, id, wt);
     const int K = a.k + a.n_shared;
-    if (lane < K) {
-        a.ids[static_cast<size_t>(t) * K + lane] = out_id;
-        a.w[static_cast<size_t>(t) * K + lane] = wt;
+    if (slot < K && in) {
+        a.ids[static_cast<size_t>(t) * K + slot] = id;
+        a.w[static_cast<size_t>(t) * K + slot] = wt;
+    }
+}
+
+// 32 warps per SM up to 256 experts (64 registers): the row's work is a chain of
+// reductions, and other warps fill its latency (16384 x 256 with groups, rows
+// weighed one by one: 18.4 us; 75 registers 20.5 us, 48 registers 19.9). A warp
+// selects one row. R rows are weighed by one warp, 32 / R lanes each: weights
+// take a fifth of a row's instructions, for k of a warp's 32 lanes. Several
+// rows selected by one warp in turn would wait longer than that saves (16384 x
+// 256: 20.7 us for 2 rows, 21.4 for 4).
+template <int N, typename L, int R>
+__global__ void __launch_bounds__(kWarpsPerBlock * 32, N <= 8 ? 8 : 1)
+route_scored_kernel(const __grid_constant__ RouterArgs a) {
+    extern __shared__ double by_all[];                           // [kWarpsPerBlock][E], only with groups
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5;
+    const int t0 = blockIdx.x * kWarpsPerBlock;
+    double *by_s = by_all + static_cast<size_t>(warp) * a.E;
+    auto row_of = [&](int t) { return static_cast<const L *>(a.logits) + static_cast<size_t>(t) * a.E; };
+    float x[N], m;
+    if constexpr (R == 1) {
+        const int t = t0 + warp;
+        if (t >= a.T) return;
+        const L *row = row_of(t);
+        const int id = select_row<N, L>(a, row, by_s, x, m);
+        weigh_row<32, L>(a, row, t, id, m, [&] { return row_sum<N>(a, x, m); });
+    } else {
+        constexpr int W = 32 / R;
+        __shared__ int ids[kWarpsPerBlock * W];
+        __shared__ float2 mz[kWarpsPerBlock];
+        if (t0 + warp < a.T) {
+            const int id = select_row<N, L>(a, row_of(t0 + warp), by_s, x, m);
+            if (lane < W) ids[warp * W + lane] = id;
+            if (a.score == MOE_SCORE_SOFTMAX && !a.renormalize) {
+                const float z = row_sum<N>(a, x, m);
+                if (lane == 0) mz[warp] = make_float2(m, z);
+            }
+        }
+        __syncthreads();
+        if (warp >= kWarpsPerBlock / R) return;
+        const int r = warp * R + lane / W;                       // this lane's row; from T on nothing of it is used
+        weigh_row<W, L>(a, row_of(t0 + r), t0 + r, ids[threadIdx.x], mz[r].x, [&] { return mz[r].y; });
     }
 }
 
@@ -685,7 +743,13 @@ cudaError_t launch_n(RouterArgs a, cudaStream_t s) {
         for (a.group_shift = 0; (1 << a.group_shift) < lanes;) ++a.group_shift;
     const int blocks = (a.T + kWarpsPerBlock - 1) / kWarpsPerBlock;
     const size_t sm = a.n_group > 1 ? static_cast<size_t>(kWarpsPerBlock) * a.E * sizeof(double) : 0;
-    return launch_pdl(route_scored_kernel<N, L>, dim3(blocks), dim3(kWarpsPerBlock * 32), sm, s, a);
+    auto kernel = route_scored_kernel<N, L, 1>;
+    if constexpr (N <= 8) {
+        const int slots = a.k + a.n_shared;
+        if (a.T >= kSharedWeighingRows && slots <= 16)
+            kernel = slots <= 8 ? route_scored_kernel<N, L, 4> : route_scored_kernel<N, L, 2>;
+    }
+    return launch_pdl(kernel, dim3(blocks), dim3(kWarpsPerBlock * 32), sm, s, a);
 }
 
 template <typename L>

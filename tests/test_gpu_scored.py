@@ -317,3 +317,29 @@ def test_binding_refuses_another_device_and_host_memory():
         moe.moe_route_scored(torch.zeros(4, 8, device=DEV), torch.zeros(8), r, sh, ids, w)
     with pytest.raises(ValueError):
         moe.moe_route_scored(torch.zeros(3, 8, device=DEV), None, r, sh, ids, w)        # too few rows
+
+
+# from 2960 rows on, rows of at most 16 slots are weighed several per warp (8 or
+# 16 lanes each): T ends a block after each count of rows, slots fill the lanes
+# or leave some, experts take each register count of a lane up to 8
+@pytest.mark.parametrize("T,E,k,n_shared", [(2960, 256, 8, 0), (2961, 128, 6, 2), (2962, 60, 4, 1), (2963, 31, 1, 0),
+                                            (3001, 160, 12, 0), (2967, 256, 15, 1), (2970, 64, 8, 1), (2959, 64, 8, 0),
+                                            (2960, 100, 16, 1), (2966, 300, 8, 0)])
+@pytest.mark.parametrize("score,renormalize", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
+@pytest.mark.parametrize("biased", [False, True], ids=["plain", "bias"])
+def test_long_calls(T, E, k, n_shared, score, renormalize, biased):
+    l = logits_of(T, E, T + E)
+    l[5] = -INF
+    l[6, : E - 1] = -INF
+    l[T - 1, ::2] = NAN
+    if T % 2:
+        l = l.to(torch.bfloat16)
+    b = bias_of(E, E) if biased else None
+    G = 4 if E % 4 == 0 and k <= E // 2 and E >= 60 else 1
+    kw = dict(score=score, renormalize=renormalize, scale=2.5, n_group=G, topk_group=max(1, G // 2), group_top=1 + biased)
+    check(l, b, k, n_shared, **kw)
+    # and as the same rows do in short calls, bit by bit
+    ids, w = run(l, b, k, n_shared, **kw)
+    for lo, hi in ((0, 9), (1000, 1007), (T - 11, T)):
+        i, v = run(l[lo:hi], b, k, n_shared, **kw)
+        assert np.array_equal(i, ids[lo:hi]) and np.array_equal(v, w[lo:hi])
