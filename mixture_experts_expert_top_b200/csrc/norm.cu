@@ -10,14 +10,16 @@
 //   MXFP8 row  per 32 elements e = floor(log2 max|y|) - 8, E4M3(y / 2^e)
 //   int8 row   scale = max|y| / 127, q = rint(y * 127 / max|y|)
 // The norm and both 8-bit forms take the fp32 values, so each output is
-// rounded once. A row lives in registers between its one read and its
+// rounded once; with MXFP8 rows y is carried past fp32 (scale_to_odd), so that
+// an E4M3 code is the formula's own. A row lives in registers between its one read and its
 // writes: the kernel's floor is the bytes of its inputs and outputs. Measured
 // (B200): norm, residual, bf16 and int8 rows of 8192 x 2048 24.5 us, 6.2 TB/s;
-// int8 rows of 65536 x 768 25.6 us, 5.9 TB/s; 256 rows of 7168 4.0 us, one row
+// int8 rows of 65536 x 768 25.6 us, 5.9 TB/s; 256 rows of 7168, bf16 and MXFP8 4.3 us, one row
 // of 2048 1.8 us (latency of the load, two reductions and the stores).
 #include <float.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "launch.h"
@@ -37,14 +39,25 @@ enum RowOut { kRowNone = 0, kRowMx = 1, kRowI8 = 2 };
 constexpr float kRoundMagic = 12582912.0f;
 
 // Sum over the TPR threads of a row, in a fixed order.
-template <int TPR>
-__device__ __forceinline__ float row_sum(float v, float *buf) {
+template <int TPR, typename F>
+__device__ __forceinline__ F row_sum(F v, F *buf) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     if constexpr (TPR > 32) {
         const int warp = threadIdx.x >> 5;
         if ((threadIdx.x & 31) == 0) buf[warp] = v;
         __syncthreads();
+        if constexpr (sizeof(F) == 8) {
+            // by halves: 64-bit additions take longer
+            F part[TPR / 32];
+#pragma unroll
+            for (int i = 0; i < TPR / 32; ++i) part[i] = buf[i];
+#pragma unroll
+            for (int n = TPR / 64; n > 0; n >>= 1)
+#pragma unroll
+                for (int i = 0; i < n; ++i) part[i] += part[i + n];
+            return part[0];
+        }
         v = buf[0];
 #pragma unroll
         for (int i = 1; i < TPR / 32; ++i) v += buf[i];
@@ -89,8 +102,27 @@ __device__ __forceinline__ uint32_t pack_low_bytes(const float *f) {
     return __byte_perm(lo, hi, 0x5410);
 }
 
+// h <- h (r + r_lo) w, rounded to odd: towards zero, and the last bit set if
+// anything was left. Rounded again, to E4M3 or bf16, that gives the product's
+// own nearest value; two fp32 products rounded to nearest put one value in 2^21
+// on the other side of one of E4M3's borders. fmaf(h, r, -p) is what p lacks of
+// h r. Past the fp32 range y is FLT_MAX: infinity in bf16, saturated in E4M3.
+// Without branches 256 rows of 7168 take 4.3 us, 4.1 with plain products, and
+// 4.7 with a branch for the values that a rounding to nearest puts on a border.
+__device__ __forceinline__ void scale_to_odd(float (&h)[8], float r, float r_lo, const float (&w)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float p = __fmul_rn(h[i], r);
+        const float t = __fmul_rn(fmaf(h[i], r_lo, fmaf(h[i], r, -p)), w[i]);
+        const float y = __fmaf_rz(p, w[i], t);
+        const float rest = fmaf(p, w[i], -y) + t;               // NaN for an infinity or NaN, which stays
+        h[i] = __uint_as_float(__float_as_uint(y) | (fabsf(rest) > 0.f ? 1u : 0u));
+    }
+}
+
 struct RowArgs {
     const uint4 *x, *residual, *weight;     // residual: null without one; weight: null without a norm
+    double inv_h;                           // 1 / row length
     float eps;
     int rows, nvec;                         // 8-element vectors per row
     uint4 *residual_out, *y;                // may be null
@@ -111,7 +143,9 @@ row_kernel(const RowArgs a) {
     constexpr bool kAhead = TPR * V <= 2048;    // longer rows need the registers for themselves
     constexpr bool kHoldWeight = kAhead && V <= 3;
     // written by one row, read until its last reduction, and the next row takes the other half
-    __shared__ float sum_s[2][kWarps], again_s[2][kWarps];
+    // MX rows: the sum over the threads (fp32 over a thread's elements) in 64 bits
+    using Sum = typename std::conditional<OUT == kRowMx, double, float>::type;
+    __shared__ Sum sum_s[2][kWarps], again_s[2][kWarps];
     __shared__ uint32_t max_s[2][kWarps];
     griddep_launch_dependents();
     griddep_wait();
@@ -151,12 +185,12 @@ row_kernel(const RowArgs a) {
         }
         if (kAhead) load(row + step);
         if constexpr (NORM) {
-            float ss = 0.f;
+            float part = 0.f;
 #pragma unroll
             for (int j = 0; j < V; ++j)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) ss = fmaf(h[j][i], h[j][i], ss);
-            ss = row_sum<TPR>(ss, sum_s[half]);
+                for (int i = 0; i < 8; ++i) part = fmaf(h[j][i], h[j][i], part);
+            Sum ss = row_sum<TPR>(static_cast<Sum>(part), sum_s[half]);
             // the outputs may be x or residual themselves: each thread writes the
             // elements that it has read
 #pragma unroll
@@ -164,22 +198,29 @@ row_kernel(const RowArgs a) {
                 const int v = t + TPR * j;
                 if (a.residual_out && v < a.nvec) a.residual_out[base + v] = pack8(h[j]);
             }
-            const float inv_h = 1.0f / static_cast<float>(a.nvec * 8);
             float eps = a.eps;
             if (!(ss <= FLT_MAX)) {
                 // squares past the fp32 range: the row and the root scaled by 2^-70
                 eps = a.eps * 0x1p-70f * 0x1p-70f;
-                ss = 0.f;
+                part = 0.f;
 #pragma unroll
                 for (int j = 0; j < V; ++j)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         h[j][i] *= 0x1p-70f;
-                        ss = fmaf(h[j][i], h[j][i], ss);
+                        part = fmaf(h[j][i], h[j][i], part);
                     }
-                ss = row_sum<TPR>(ss, again_s[half]);
+                ss = row_sum<TPR>(static_cast<Sum>(part), again_s[half]);
             }
-            const float rstd = 1.0f / sqrtf(fmaf(ss, inv_h, eps));
+            const Sum mean = fma(ss, static_cast<Sum>(a.inv_h), static_cast<Sum>(eps));
+            const float rstd = 1.0f / sqrtf(static_cast<float>(mean));
+            float rstd_lo = 0.f;                                // MX rows: 1 / sqrt(mean) - rstd, a Newton step
+            if constexpr (OUT == kRowMx) {
+                if (rstd > 0.f && rstd <= FLT_MAX) {
+                    const double r = rstd;
+                    rstd_lo = static_cast<float>(0.5 * r * fma(-mean * r, r, 1.0));
+                }
+            }
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const int v = t + TPR * j;
@@ -187,7 +228,10 @@ row_kernel(const RowArgs a) {
                     float w[8];
                     unpack8(kHoldWeight ? wv[j] : __ldg(a.weight + v), w);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) h[j][i] = h[j][i] * rstd * w[i];
+                    for (int i = 0; i < 8; ++i) {
+                        if constexpr (OUT != kRowMx) h[j][i] = h[j][i] * rstd * w[i];
+                    }
+                    if constexpr (OUT == kRowMx) scale_to_odd(h[j], rstd, rstd_lo, w);
                     if (a.y) a.y[base + v] = pack8(h[j]);
                 }
             }
@@ -335,6 +379,7 @@ cudaError_t launch_rmsnorm(const NormArgs &n, cudaStream_t s) {
     a.eps = n.eps;
     a.rows = n.rows;
     a.nvec = n.H / 8;
+    a.inv_h = 1.0 / n.H;
     a.residual_out = reinterpret_cast<uint4 *>(n.residual_out);
     a.y = reinterpret_cast<uint4 *>(n.y);
     a.q = reinterpret_cast<uint2 *>(n.q);
