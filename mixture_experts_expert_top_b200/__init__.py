@@ -248,12 +248,29 @@ def _addresses(dev: int, *spec):
             raise ValueError("tensors passed to libmoe_b200 must be contiguous")
         if t.numel() < n:
             raise ValueError(f"libmoe_b200: expected at least {n} elements, got a tensor of shape {tuple(t.shape)}")
+    for t, n, code in given:
         if t.get_device() != dev:
             raise ValueError(f"libmoe_b200: expected a tensor on the current CUDA device, got one on {t.device}")
     raise RuntimeError("libmoe_b200: a tensor was refused")
 
 
 _checked = _addresses          # _marshal.addresses from the first call on
+
+# by format, per weight row of K elements: codes, scales, and their types
+_WEIGHT_ROWS = {FMT_BF16: (lambda K: K, lambda K: 0, _BF16, _BF16),
+                FMT_INT4_G128: (lambda K: K // 2, lambda K: K // 128, _U8, _BF16),
+                FMT_MXFP8: (lambda K: K, lambda K: K // 32, _U8, _U8),
+                FMT_MXFP4: (lambda K: K // 2, lambda K: K // 32, _U8, _U8),
+                FMT_INT8: (lambda K: K, lambda K: 1, _I8, _F32)}
+
+
+def _weights(shape: Shape, w_gu, w_gu_scales, w_d, w_d_scales):
+    """The layer's weights as _addresses takes them."""
+    _, H, I, E, _, fmt, S = _dims(shape)
+    codes, scales, w_type, s_type = _WEIGHT_ROWS[fmt]
+    gu, dn = (E + S) * 2 * I, (E + S) * H
+    return (w_gu, gu * codes(H), w_type, w_gu_scales, gu * scales(H), s_type,
+            w_d, dn * codes(I), w_type, w_d_scales, dn * scales(I), s_type)
 
 
 _cuda_used = False
@@ -375,20 +392,30 @@ def moe_finalize(y, topk_w, inv_perm, shape, out, stream=None) -> None:
 
 
 def moe_forward(hidden, logits, w_gu, w_gu_scales, w_d, w_d_scales, shape, out, ws, stream=None) -> None:
-    nbytes = ws.numel() * ws.element_size()
-    _check(lib().moe_forward(_p(hidden, BF16), _p(logits, F32), _p(w_gu, BF16, U8, I8), _p(w_gu_scales, BF16, U8, F32),
-                             _p(w_d, BF16, U8, I8), _p(w_d_scales, BF16, U8, F32), ctypes.byref(_shape(shape)), _p(out, BF16),
-                             _p(ws), nbytes, _s(stream)),
-           "moe_forward")
+    nbytes, sh = ws.numel() * ws.element_size(), _shape(shape)
+    if sh.fmt == FMT_INT8:
+        d = _dev()
+        spec = (hidden, sh.T * sh.H, _BF16, logits, sh.T * sh.E, _F32, *_weights(sh, w_gu, w_gu_scales, w_d, w_d_scales),
+                out, sh.T * sh.H, _BF16)
+        ph, pl, pg, pgs, pd, pds, po = _checked(d, *spec) or _addresses(d, *spec)
+    else:
+        ph, pl, pg, pgs = _p(hidden, BF16), _p(logits, F32), _p(w_gu, BF16, U8), _p(w_gu_scales, BF16, U8)
+        pd, pds, po = _p(w_d, BF16, U8), _p(w_d_scales, BF16, U8), _p(out, BF16)
+    _check(lib().moe_forward(ph, pl, pg, pgs, pd, pds, ctypes.byref(sh), po, _p(ws), nbytes, _s(stream)), "moe_forward")
 
 
 def moe_forward_host(hidden_host, logits_host, w_gu, w_gu_scales, w_d, w_d_scales, shape, out_host, ws,
                      stream=None) -> None:
-    nbytes = ws.numel() * ws.element_size()
-    _check(lib().moe_forward_host(_p(hidden_host, BF16), _p(logits_host, F32), _p(w_gu, BF16, U8, I8),
-                                  _p(w_gu_scales, BF16, U8, F32), _p(w_d, BF16, U8, I8),
-                                  _p(w_d_scales, BF16, U8, F32),
-                                  ctypes.byref(_shape(shape)), _p(out_host, BF16), _p(ws), nbytes, _s(stream)),
+    nbytes, sh = ws.numel() * ws.element_size(), _shape(shape)
+    if sh.fmt == FMT_INT8:
+        d = _dev()
+        spec = _weights(sh, w_gu, w_gu_scales, w_d, w_d_scales)
+        pg, pgs, pd, pds = _checked(d, *spec) or _addresses(d, *spec)
+    else:
+        pg, pgs = _p(w_gu, BF16, U8), _p(w_gu_scales, BF16, U8)
+        pd, pds = _p(w_d, BF16, U8), _p(w_d_scales, BF16, U8)
+    _check(lib().moe_forward_host(_p(hidden_host, BF16), _p(logits_host, F32), pg, pgs, pd, pds, ctypes.byref(sh),
+                                  _p(out_host, BF16), _p(ws), nbytes, _s(stream)),
            "moe_forward_host")
 
 
@@ -449,20 +476,11 @@ def moe_grouped_gemm_down_i8(act_q, act_scales, offsets, w_d, w_d_scales, shape,
 def moe_forward_scored(hidden, logits, bias, router: Router, w_gu, w_gu_scales, w_d, w_d_scales, shape, out, ws,
                        stream=None) -> None:
     sh, d = _shape(shape), _dev()
-    T, H, I, E, _, fmt, S = _dims(sh)
-    Et = E + S
-    # per weight row of K elements: codes and scales, and their types
-    row = {FMT_BF16: (lambda K: K, lambda K: 0, _BF16, _BF16),
-           FMT_INT4_G128: (lambda K: K // 2, lambda K: K // 128, _U8, _BF16),
-           FMT_MXFP8: (lambda K: K, lambda K: K // 32, _U8, _U8),
-           FMT_MXFP4: (lambda K: K // 2, lambda K: K // 32, _U8, _U8),
-           FMT_INT8: (lambda K: K, lambda K: 1, _I8, _F32)}
-    if fmt not in row:
+    T, H, _, E, _, fmt, _ = _dims(sh)
+    if fmt not in _WEIGHT_ROWS:
         raise MoeError(1, "moe_forward_scored")
-    codes, scales, w_type, s_type = row[fmt]
     spec = (hidden, T * H, _BF16, logits, T * E, _BF16 if router.logits else _F32, bias, E, _F32,
-            w_gu, Et * 2 * I * codes(H), w_type, w_gu_scales, Et * 2 * I * scales(H), s_type,
-            w_d, Et * H * codes(I), w_type, w_d_scales, Et * H * scales(I), s_type, out, T * H, _BF16, ws, 0, _U8)
+            *_weights(sh, w_gu, w_gu_scales, w_d, w_d_scales), out, T * H, _BF16, ws, 0, _U8)
     ph, pl, pb, pg, pgs, pd, pds, po, pws = _checked(d, *spec) or _addresses(d, *spec)
     _check(lib().moe_forward_scored(ph, pl, pb, router, pg, pgs, pd, pds, sh, po, pws, ws.numel(), _s(stream, d)),
            "moe_forward_scored")

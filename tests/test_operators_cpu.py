@@ -194,6 +194,78 @@ def test_binding_refuses_tensors_it_cannot_pass():
         moe.forward(bf, torch.zeros(4, 8), bf, bf, 2, bias=torch.zeros(8))          # a bias without a router
 
 
+# ---- the layer's weights: types and sizes by format ---------------------------
+
+LAYER = (4, 256, 128, 8, 2)          # T, H, I, E, top_k
+
+
+def layer_call(which, fmt, codes, scales):
+    """One call of a layer entry point with weights of these types; `scales` may also be a function of the number of
+    scales per weight array (an array of another length)."""
+    T, H, I, E, k = LAYER
+    per = {"bf16": (1, 0), "int4_g128": (2, 128), "mxfp8": (1, 32), "mxfp4": (2, 32), "int8": (1, None)}[fmt]
+
+    def weights(rows, K):
+        n = rows * (1 if per[1] is None else K // per[1] if per[1] else 0)
+        w = torch.zeros(rows * (K // per[0]), dtype=codes)
+        return w, scales(n) if callable(scales) else torch.zeros(n, dtype=scales)
+
+    w_gu, gs = weights(E * 2 * I, H)
+    w_d, ds = weights(E * H, I)
+    hidden, logits, out = torch.zeros(T, H, dtype=torch.bfloat16), torch.zeros(T, E), torch.zeros(T, H, dtype=torch.bfloat16)
+    sh = moe.Shape.of(*LAYER, fmt)
+    ws = torch.zeros(1 << 20, dtype=torch.uint8)
+    if which == "forward":
+        return moe.forward(hidden, logits, w_gu.view(E, 2 * I, -1), w_d.view(E, H, -1), k, gs.view(E, 2 * I, -1),
+                           ds.view(E, H, -1), out=out, ws=ws, stream=0)
+    f = moe.moe_forward if which == "moe_forward" else moe.moe_forward_host
+    return f(hidden, logits, w_gu, gs, w_d, ds, sh, out, ws, stream=0)
+
+
+@pytest.fixture
+def library_not_reached(monkeypatch):
+    class Stub:
+        def __getattr__(self, name):
+            if name == "moe_workspace_size":
+                return lambda *a: 1 << 20
+            raise AssertionError(f"{name} was called")
+    monkeypatch.setattr(moe, "lib", lambda: Stub())
+
+
+@pytest.mark.parametrize("which", ["moe_forward", "moe_forward_host"])
+@pytest.mark.parametrize("fmt,codes,scales", [
+    ("int4_g128", torch.int8, torch.float32), ("int4_g128", torch.uint8, torch.float32),
+    ("int4_g128", torch.int8, torch.bfloat16), ("mxfp8", torch.int8, torch.uint8), ("mxfp4", torch.uint8, torch.float32),
+    ("bf16", torch.int8, torch.bfloat16), ("int8", torch.int8, torch.bfloat16), ("int8", torch.uint8, torch.float32),
+    ("int8", torch.bfloat16, torch.float32), ("int8", torch.int8, torch.uint8)])
+def test_layer_refuses_another_formats_weights(library_not_reached, which, fmt, codes, scales):
+    with pytest.raises(TypeError):
+        layer_call(which, fmt, codes, scales)
+
+
+@pytest.mark.parametrize("which", ["moe_forward", "moe_forward_host", "forward"])
+def test_int8_layer_refuses_short_scales_and_bf16_scales(library_not_reached, which):
+    # the kernels read one fp32 scale per weight row: fewer, or 16-bit ones, would be read past their end
+    with pytest.raises(TypeError):
+        layer_call(which, "int8", torch.int8, torch.bfloat16)
+    if which != "forward":
+        with pytest.raises(ValueError, match="at least"):
+            layer_call(which, "int8", torch.int8, lambda n: torch.zeros(4))
+    with pytest.raises(ValueError, match="current CUDA device"):
+        layer_call(which, "int8", torch.int8, torch.float32)
+
+
+def test_int8_layer_refuses_short_activations(library_not_reached):
+    T, H, I, E, k = LAYER
+    w_gu, w_d = torch.zeros(E, 2 * I, H, dtype=torch.int8), torch.zeros(E, H, I, dtype=torch.int8)
+    gs, ds = torch.zeros(E, 2 * I), torch.zeros(E, H)
+    x, l, ws = torch.zeros(T, H, dtype=torch.bfloat16), torch.zeros(T, E), torch.zeros(64, dtype=torch.uint8)
+    sh = moe.Shape.of(*LAYER, "int8")
+    for hidden, logits, out in ((x[1:], l, x), (x, l[1:], x), (x, l, x[1:])):
+        with pytest.raises(ValueError, match="at least"):
+            moe.moe_forward(hidden, logits, w_gu, gs, w_d, ds, sh, out, ws, stream=0)
+
+
 def test_router_struct_has_the_c_layout():
     assert [f[0] for f in moe.Router._fields_] == ["logits", "score", "n_group", "topk_group", "group_top",
                                                    "renormalize", "scale"]
