@@ -198,29 +198,34 @@ row_kernel(const RowArgs a) {
                 const int v = t + TPR * j;
                 if (a.residual_out && v < a.nvec) a.residual_out[base + v] = pack8(h[j]);
             }
-            float eps = a.eps;
+            float eps = a.eps, back = 1.0f;
             if (!(ss <= FLT_MAX)) {
-                // squares past the fp32 range: the row and the root scaled by 2^-70
-                eps = a.eps * 0x1p-70f * 0x1p-70f;
+                // squares past the fp32 range: those of h 2^-80, whose sum over a row is at
+                // most 2^15 2^96; the root is scaled back in two factors of 2^-40, so that
+                // neither h nor 1 / root leaves the normal range
+                eps = a.eps * 0x1p-80f * 0x1p-80f;
+                back = 0x1p-40f;
                 part = 0.f;
 #pragma unroll
                 for (int j = 0; j < V; ++j)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        h[j][i] *= 0x1p-70f;
-                        part = fmaf(h[j][i], h[j][i], part);
+                        const float small = h[j][i] * 0x1p-80f;
+                        part = fmaf(small, small, part);
+                        h[j][i] *= 0x1p-40f;
                     }
                 ss = row_sum<TPR>(static_cast<Sum>(part), again_s[half]);
             }
             const Sum mean = fma(ss, static_cast<Sum>(a.inv_h), static_cast<Sum>(eps));
-            const float rstd = 1.0f / sqrtf(static_cast<float>(mean));
+            float rstd = 1.0f / sqrtf(static_cast<float>(mean));
             float rstd_lo = 0.f;                                // MX rows: 1 / sqrt(mean) - rstd, a Newton step
             if constexpr (OUT == kRowMx) {
                 if (rstd > 0.f && rstd <= FLT_MAX) {
                     const double r = rstd;
-                    rstd_lo = static_cast<float>(0.5 * r * fma(-mean * r, r, 1.0));
+                    rstd_lo = back * static_cast<float>(0.5 * r * fma(-mean * r, r, 1.0));
                 }
             }
+            rstd *= back;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const int v = t + TPR * j;

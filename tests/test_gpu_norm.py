@@ -241,3 +241,26 @@ def test_mxfp8_codes_equal_the_formulas(rows, H):
     want = ((v / step).round() * step).clamp(-448, 448).view(rows, H)
     code = got["q"].view(torch.float8_e4m3fn).double()
     assert int((code != want).sum()) == 0
+
+
+@pytest.mark.parametrize("H", [4096, 7168, 8192, 16384, 32768])
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8", "int8"])
+def test_long_rows_of_the_largest_values(H, fmt):
+    """Squares whose sum is past the fp32 range by up to 2^143: H values of
+    nearly 2^128."""
+    top = torch.finfo(torch.bfloat16).max
+    x, _, w = inputs(7, H, residual=False)
+    sign = torch.where(torch.arange(H, device=DEV) % 3 == 0, -1.0, 1.0)
+    x[0] = top
+    x[1] = (sign * top).to(torch.bfloat16)
+    x[2] = 1.6e38
+    x[3] = 3e36
+    x[4] = x[4] * 2.0 ** 20; x[4, 5] = top                        # ordinary values beside one such: y near 2^-100
+    x[5, : H // 2] = 0; x[5, H // 2:] = -top
+    got = check(x, None, w, fmt)
+    if fmt == "bf16":
+        assert torch.equal(got["y"][0], w)                        # (1 + 2^-18) w rounds to w: 8 bits
+    # and as h: zeros, then with a residual of the same size and sign that stays below infinity
+    half = (sign * 1.6e38).to(torch.bfloat16).expand(7, H).contiguous()
+    check(torch.zeros_like(half), half, w, fmt)
+    check(half, half, w, fmt)
