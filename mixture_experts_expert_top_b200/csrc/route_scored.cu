@@ -494,8 +494,9 @@ __device__ __forceinline__ int select_choices(const RouterArgs &a, const L *row,
     const float unit = kSteps / (hi - lo);
     // twice the error and the two keys' rounding, one step each
     const float gap = ceilf(2.0f * err * unit) + 3.0f;
-    // one value, an infinity, or a range that the grid does not resolve: not here
-    const bool grid_ok = lo < hi && hi < INFINITY && unit < 3e37f && gap < 0.125f * kSteps;
+    // one value, an infinity, a span past the fp32 range (unit 0, and c - lo infinite), or a
+    // range that the grid does not resolve: not here
+    const bool grid_ok = lo < hi && hi - lo < INFINITY && unit < 3e37f && gap < 0.125f * kSteps;
     if (a.n_group > 1 && (gs < 0 || !grid_ok)) {
         bool sure = true;
         bits = kept_experts<N>(a, c, err, reinterpret_cast<float *>(by_s), sure);

@@ -343,3 +343,25 @@ def test_long_calls(T, E, k, n_shared, score, renormalize, biased):
     for lo, hi in ((0, 9), (1000, 1007), (T - 11, T)):
         i, v = run(l[lo:hi], b, k, n_shared, **kw)
         assert np.array_equal(i, ids[lo:hi]) and np.array_equal(v, w[lo:hi])
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G", [(64, 8), (60, 5), (256, 8)])
+def test_groups_whose_biases_span_more_than_the_fp32_range(score, E, G):
+    # a group's two largest choices may cancel (3e38 - 3e38 = 0 in 64 bits) or add past
+    # the fp32 range, and the choices' span hi - lo is past it too
+    l = logits_of(40, E, 7)
+    size = E // G
+    b = torch.zeros(E)
+    b[0] = 3e38
+    b[1:size] = -3e38                                        # group 0: 0, below every s1 + s2 > 0
+    for k, keep, top in ((4, 2, 2), (2, 1, 2), (4, 2, 1), (6, G - 1, 2)):
+        check(l, b, k, score=score, n_group=G, topk_group=keep, group_top=top)
+    b[size] = 2e38                                           # group 1: 2e38, its second one near 0
+    check(l, b, 4, score=score, n_group=G, topk_group=1, group_top=2)
+    b[2 * size:2 * size + 2] = 3e38                          # group 2: 6e38
+    b[3 * size:4 * size] = -3e38                             # group 3: -6e38
+    b[3 * size] = -INF
+    for keep in (1, 2, G - 1, G):
+        check(l, b, 4, score=score, n_group=G, topk_group=keep, group_top=2)
+    check(l, b, 8, score=score)                              # without groups
