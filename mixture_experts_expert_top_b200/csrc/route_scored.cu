@@ -669,8 +669,17 @@ __device__ __forceinline__ void weigh_row(const RouterArgs &a, const L *row, int
         s = (l == m ? 1.0f : expf(l - m)) / z;
     } else if (soft || (a.renormalize && lmax < -60.0f)) {
         s = l == lmax ? 1.0f : expf(l - lmax);
+    } else if (a.renormalize) {
+        // times 2^100, which the quotient does not see: below -60 s is exp(l) to fp32, as the
+        // square of its root, and neither leaves the normal range before the weight does
+        const bool low = l < -60.0f;
+        const float e = expf(low ? 0.5f * l : -l);
+        s = low ? (e * 0x1p50f) * (e * 0x1p50f) : fast_rcp(1.0f + e) * 0x1p100f;
     } else {
-        s = fast_rcp(1.0f + expf(-l));
+        // below -60 s is exp(l) to fp32; from -87.3 on the reciprocal would flush it to 0
+        const bool low = l < -60.0f;
+        const float e = expf(low ? l : -l);
+        s = low ? e : fast_rcp(1.0f + e);
     }
     if (off || l == -INFINITY || !live) s = 0.f;
     float wt = s;

@@ -365,3 +365,18 @@ def test_groups_whose_biases_span_more_than_the_fp32_range(score, E, G):
     for keep in (1, 2, G - 1, G):
         check(l, b, 4, score=score, n_group=G, topk_group=keep, group_top=2)
     check(l, b, 8, score=score)                              # without groups
+
+
+@pytest.mark.parametrize("T", [40, 3000])
+def test_sigmoid_weights_of_scores_near_and_below_the_smallest_normal(T):
+    # s = exp(l) from 2^-83 down to 2^-150: as they are, and relative to a selected
+    # score that is larger by any factor
+    E, k = 64, 8
+    l = torch.full((T, E), -120.0)
+    l[:, :k] = -60.0 - 44.0 * torch.rand(T, k, generator=torch.Generator().manual_seed(1))
+    check(l, None, k, score="sigmoid", renormalize=False)
+    check(l, None, k, score="sigmoid")
+    for top in (-59.0, -50.0, -61.0, -20.0, 3.0):
+        l[:, 3] = top
+        check(l, None, k, score="sigmoid")
+        check(l, None, k, score="sigmoid", renormalize=False)
