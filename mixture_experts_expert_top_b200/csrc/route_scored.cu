@@ -751,7 +751,7 @@ cudaError_t launch_n(RouterArgs a, cudaStream_t s) {
     a.group_shift = -1;
     if (size % N == 0 && (lanes & (lanes - 1)) == 0)
         for (a.group_shift = 0; (1 << a.group_shift) < lanes;) ++a.group_shift;
-    const int blocks = (a.T + kWarpsPerBlock - 1) / kWarpsPerBlock;
+    const int blocks = (a.T - 1) / kWarpsPerBlock + 1;           // T up to 2^31 - 1
     const size_t sm = a.n_group > 1 ? static_cast<size_t>(kWarpsPerBlock) * a.E * sizeof(double) : 0;
     auto kernel = route_scored_kernel<N, L, 1>;
     if constexpr (N <= 8) {

@@ -380,3 +380,14 @@ def test_sigmoid_weights_of_scores_near_and_below_the_smallest_normal(T):
         l[:, 3] = top
         check(l, None, k, score="sigmoid")
         check(l, None, k, score="sigmoid", renormalize=False)
+
+
+def test_as_many_rows_as_a_shape_allows():
+    T = 2 ** 31 - 1
+    l = torch.zeros(T, 1, dtype=torch.bfloat16, device=DEV)
+    ids = torch.full((T, 1), -7, dtype=torch.int32, device=DEV)
+    w = torch.empty(T, 1, device=DEV)
+    moe.moe_route_scored(l, None, moe.Router.of(logits="bf16"), moe.Shape.of(T, 8, 8, 1, 1), ids, w)
+    torch.cuda.synchronize()
+    for lo in range(0, T, 2 ** 28):
+        assert bool((ids[lo:lo + 2 ** 28] == 0).all()) and bool((w[lo:lo + 2 ** 28] == 1).all())
