@@ -13,9 +13,10 @@
 // rounded once; with MXFP8 rows y is carried past fp32 (scale_to_odd), so that
 // an E4M3 code is the formula's own. A row lives in registers between its one read and its
 // writes: the kernel's floor is the bytes of its inputs and outputs. Measured
-// (B200): norm, residual, bf16 and int8 rows of 8192 x 2048 24.5 us, 6.2 TB/s;
-// int8 rows of 65536 x 768 25.6 us, 5.9 TB/s; 256 rows of 7168, bf16 and MXFP8 4.3 us, one row
-// of 2048 1.8 us (latency of the load, two reductions and the stores).
+// (B200): norm, residual, bf16 and int8 rows of 8192 x 2048 24.1 us, 6.3 TB/s,
+// with MXFP8 rows 25.8 us; int8 rows of 65536 x 768 24.6 us, 6.1 TB/s; 256 rows of
+// 7168, bf16 and MXFP8, 4.5 us; one row of 2048 1.5 us, MXFP8 1.9 (latency of the
+// load, two reductions and the stores).
 #include <float.h>
 
 #include <algorithm>
@@ -102,21 +103,103 @@ __device__ __forceinline__ uint32_t pack_low_bytes(const float *f) {
     return __byte_perm(lo, hi, 0x5410);
 }
 
+// Two floats as the operands of packed arithmetic: half the instructions.
+struct Pair {
+    float x, y;
+};
+__device__ __forceinline__ uint64_t bits(Pair p) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(p.x), "f"(p.y));
+    return r;
+}
+__device__ __forceinline__ Pair pair_of(uint64_t b) {
+    Pair p;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(p.x), "=f"(p.y) : "l"(b));
+    return p;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+    return pair_of(r);
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+    return pair_of(r);
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+    return pair_of(r);
+}
+__device__ __forceinline__ Pair fma2_rz(Pair a, Pair b, Pair c) {
+    uint64_t r;
+    asm("fma.rz.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+    return pair_of(r);
+}
+
+// Sum of the squares of a thread's elements times f (a power of two). As a
+// float, an fp32 chain. As a double, what the chain's roundings drop is summed
+// beside it (two chains, of even and odd elements): with s at least as large as
+// the next square, t = fl(s + h^2) is at most 2 s, so s - t is exact and h^2 + (s -
+// t) is what is missing. s starts at the largest square, rounded up, for that.
+// Each chain's at most 32 squares are kept to 2^-37 of their sum at worst, to
+// about 2^-45 as roundings go both ways. MXFP8 rows need it: with fp32 chains 10
+// codes of 32 million fell on the other side of a border of E4M3. It takes 0.1
+// us of a row of 2048 and of 256 rows of 7168, 0.7 of 8192 x 2048.
+template <typename Sum, int V>
+__device__ __forceinline__ Sum square_sum(const float (&h)[V][8], float f) {
+    if constexpr (sizeof(Sum) == 8) {
+        float top = 0.f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            float m[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m[i] = fmaxf(fabsf(h[j][2 * i]), fabsf(h[j][2 * i + 1]));
+            top = fmaxf(top, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
+        }
+        top *= f;
+        const float first = __fmul_ru(top, top);
+        Pair s = {first, first}, lo = {0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                const Pair x = {h[j][i] * f, h[j][i + 1] * f};
+                const Pair t = fma2(x, x, s);
+                lo = add2(lo, fma2(x, x, fma2(t, {-1.0f, -1.0f}, s)));
+                s = t;
+            }
+        const Sum sum = static_cast<Sum>(s.x) + s.y;
+        return sum <= 2.0 * FLT_MAX ? sum - 2.0 * first + (lo.x + lo.y) : sum;
+    } else {
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s = fmaf(h[j][i] * f, h[j][i] * f, s);
+        return s;
+    }
+}
+
 // h <- h (r + r_lo) w, rounded to odd: towards zero, and the last bit set if
 // anything was left. Rounded again, to E4M3 or bf16, that gives the product's
 // own nearest value; two fp32 products rounded to nearest put one value in 2^21
-// on the other side of one of E4M3's borders. fmaf(h, r, -p) is what p lacks of
+// on the other side of one of E4M3's borders. fma(h, r, -p) is what p lacks of
 // h r. Past the fp32 range y is FLT_MAX: infinity in bf16, saturated in E4M3.
-// Without branches 256 rows of 7168 take 4.3 us, 4.1 with plain products, and
-// 4.7 with a branch for the values that a rounding to nearest puts on a border.
+// With square_sum's exact sum 256 rows of 7168 take 4.48 us, 8192 x 2048 25.8
+// and a row of 2048 1.92; plain products of fp32 sums 4.08, 24.2 and 1.60. A
+// branch for the values that a rounding to nearest puts on a border took longer.
 __device__ __forceinline__ void scale_to_odd(float (&h)[8], float r, float r_lo, const float (&w)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float p = __fmul_rn(h[i], r);
-        const float t = __fmul_rn(fmaf(h[i], r_lo, fmaf(h[i], r, -p)), w[i]);
-        const float y = __fmaf_rz(p, w[i], t);
-        const float rest = fmaf(p, w[i], -y) + t;               // NaN for an infinity or NaN, which stays
-        h[i] = __uint_as_float(__float_as_uint(y) | (fabsf(rest) > 0.f ? 1u : 0u));
+    for (int i = 0; i < 8; i += 2) {
+        const Pair x = {h[i], h[i + 1]}, v = {w[i], w[i + 1]};
+        const Pair p = mul2(x, {r, r}), minus_p = mul2(x, {-r, -r});
+        const Pair t = mul2(fma2(x, {r_lo, r_lo}, fma2(x, {r, r}, minus_p)), v);
+        const Pair y = fma2_rz(p, v, t);
+        const Pair rest = fma2(t, {-1.0f, -1.0f}, fma2(minus_p, v, y));      // NaN for an infinity or NaN, which stays
+        h[i] = __uint_as_float(__float_as_uint(y.x) | (fabsf(rest.x) > 0.f ? 1u : 0u));
+        h[i + 1] = __uint_as_float(__float_as_uint(y.y) | (fabsf(rest.y) > 0.f ? 1u : 0u));
     }
 }
 
@@ -143,7 +226,6 @@ row_kernel(const RowArgs a) {
     constexpr bool kAhead = TPR * V <= 2048;    // longer rows need the registers for themselves
     constexpr bool kHoldWeight = kAhead && V <= 3;
     // written by one row, read until its last reduction, and the next row takes the other half
-    // MX rows: the sum over the threads (fp32 over a thread's elements) in 64 bits
     using Sum = typename std::conditional<OUT == kRowMx, double, float>::type;
     __shared__ Sum sum_s[2][kWarps], again_s[2][kWarps];
     __shared__ uint32_t max_s[2][kWarps];
@@ -185,12 +267,7 @@ row_kernel(const RowArgs a) {
         }
         if (kAhead) load(row + step);
         if constexpr (NORM) {
-            float part = 0.f;
-#pragma unroll
-            for (int j = 0; j < V; ++j)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) part = fmaf(h[j][i], h[j][i], part);
-            Sum ss = row_sum<TPR>(static_cast<Sum>(part), sum_s[half]);
+            Sum ss = row_sum<TPR>(square_sum<Sum>(h, 1.0f), sum_s[half]);
             // the outputs may be x or residual themselves: each thread writes the
             // elements that it has read
 #pragma unroll
@@ -205,16 +282,11 @@ row_kernel(const RowArgs a) {
                 // neither h nor 1 / root leaves the normal range
                 eps = a.eps * 0x1p-80f * 0x1p-80f;
                 back = 0x1p-40f;
-                part = 0.f;
+                ss = row_sum<TPR>(square_sum<Sum>(h, 0x1p-80f), again_s[half]);
 #pragma unroll
                 for (int j = 0; j < V; ++j)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float small = h[j][i] * 0x1p-80f;
-                        part = fmaf(small, small, part);
-                        h[j][i] *= 0x1p-40f;
-                    }
-                ss = row_sum<TPR>(static_cast<Sum>(part), again_s[half]);
+                    for (int i = 0; i < 8; ++i) h[j][i] *= 0x1p-40f;
             }
             const Sum mean = fma(ss, static_cast<Sum>(a.inv_h), static_cast<Sum>(eps));
             float rstd = 1.0f / sqrtf(static_cast<float>(mean));
