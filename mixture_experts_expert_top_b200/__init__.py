@@ -15,6 +15,8 @@ a router by scores and an RMS norm beside it
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import struct
 from typing import Optional
@@ -232,10 +234,12 @@ def _addresses(dev: int, *spec):
             try:
                 _build.build_marshal()
             except Exception as e:      # noqa: BLE001 - re-raised with the path
-                raise RuntimeError(f"{_build.MARSHAL} is missing or older than its source and could not be "
+                raise RuntimeError(f"{_build.marshal_file()} is missing or older than its source and could not be "
                                    f"built ({e}): build it with `python -m mixture_experts_expert_top_b200.build`")
-        from . import _marshal
-        _checked = _marshal.addresses
+        loader = importlib.machinery.ExtensionFileLoader(f"{__name__}._marshal", _build.marshal_file())
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader(loader.name, loader))
+        loader.exec_module(module)
+        _checked = module.addresses
     found = _checked(dev, *spec)
     if found is not None:
         return found
@@ -254,7 +258,7 @@ def _addresses(dev: int, *spec):
     raise RuntimeError("libmoe_b200: a tensor was refused")
 
 
-_checked = _addresses          # _marshal.addresses from the first call on
+_checked = _addresses          # the _marshal module's from the first call on
 
 # by format, per weight row of K elements: codes, scales, and their types
 _WEIGHT_ROWS = {FMT_BF16: (lambda K: K, lambda K: 0, _BF16, _BF16),

@@ -1,5 +1,5 @@
 """Build libmoe_b200.so (CUDA C++ for sm_100a) in-tree with nvcc, and the
-binding's tensor checks (_marshal.so, C++ against Python and torch) with g++.
+binding's tensor checks (_marshal, C++ against Python and torch) with g++.
 
 The library is plain CUDA: no torch headers, no Python symbols. It links the
 CUDA runtime statically and reaches the driver's cuTensorMapEncodeTiled
@@ -21,7 +21,6 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libmoe_b200.so")
 LIB_DEBUG = os.path.join(HERE, "libmoe_b200_debug.so")
-MARSHAL = os.path.join(HERE, "_marshal.so")
 MARSHAL_SOURCE = os.path.join(CSRC, "marshal.cpp")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
@@ -59,14 +58,25 @@ def up_to_date(debug_bounds: bool = False) -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
+def marshal_file() -> str:
+    """The tensor checks' module for this Python and this torch: it is compiled
+    against the insides of both, so neither loads the other's."""
+    import sysconfig
+
+    import torch
+    return os.path.join(HERE, f"_marshal.torch-{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
 def marshal_up_to_date() -> bool:
-    return os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL_SOURCE) <= os.path.getmtime(MARSHAL)
+    path = marshal_file()
+    return os.path.exists(path) and os.path.getmtime(MARSHAL_SOURCE) <= os.path.getmtime(path)
 
 
 def build_marshal(force: bool = False, verbose: bool = False) -> str:
-    """Compiles csrc/marshal.cpp into _marshal.so (g++, torch's headers)."""
+    """Compiles csrc/marshal.cpp into marshal_file() (g++, torch's headers)."""
+    path = marshal_file()
     if not force and marshal_up_to_date():
-        return MARSHAL
+        return path
     import sysconfig
 
     import torch
@@ -75,12 +85,12 @@ def build_marshal(force: bool = False, verbose: bool = False) -> str:
     cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I", sysconfig.get_paths()["include"], "-I", os.path.join(root, "include"), "-I", "/usr/local/cuda/include",
-           MARSHAL_SOURCE, "-o", MARSHAL + ".tmp", "-L", lib, f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10"]
+           MARSHAL_SOURCE, "-o", path + ".tmp", "-L", lib, f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10"]
     if verbose:
         print(" ".join(cmd))
     subprocess.run(cmd, check=True)
-    os.replace(MARSHAL + ".tmp", MARSHAL)
-    return MARSHAL
+    os.replace(path + ".tmp", path)
+    return path
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False, debug_bounds: bool = False) -> str:

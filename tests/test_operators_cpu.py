@@ -272,6 +272,14 @@ def test_router_struct_has_the_c_layout():
     assert ctypes.sizeof(moe.Router) == 28
 
 
+def test_marshal_module_belongs_to_one_torch_and_python(monkeypatch):
+    # it reads at::Tensor's internals: with another torch, the file of this one is not up to date
+    moe_build.build_marshal()
+    assert moe_build.marshal_up_to_date()
+    monkeypatch.setattr(torch, "__version__", "0.0.0+other")
+    assert not moe_build.marshal_up_to_date()
+
+
 # ---- the plain forms themselves ---------------------------------------------
 
 def test_plain_router_by_hand():
