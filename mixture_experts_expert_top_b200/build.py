@@ -82,14 +82,19 @@ def build_marshal(force: bool = False, verbose: bool = False) -> str:
     import torch
     root = os.path.join(os.path.dirname(torch.__file__))
     lib = os.path.join(root, "lib")
+    tmp = f"{path}.{os.urandom(8).hex()}.tmp"   # several ranks may build at once
     cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I", sysconfig.get_paths()["include"], "-I", os.path.join(root, "include"), "-I", "/usr/local/cuda/include",
-           MARSHAL_SOURCE, "-o", path + ".tmp", "-L", lib, f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10"]
+           MARSHAL_SOURCE, "-o", tmp, "-L", lib, f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10"]
     if verbose:
         print(" ".join(cmd))
-    subprocess.run(cmd, check=True)
-    os.replace(path + ".tmp", path)
+    try:
+        subprocess.run(cmd, check=True)
+        os.replace(tmp, path)
+    finally:
+        if os.path.exists(tmp):
+            os.remove(tmp)
     return path
 
 

@@ -4,6 +4,7 @@ enqueued (no GPU needed, addresses are never used), and the plain forms that
 the GPU tests compare with."""
 
 import ctypes
+import os
 
 import numpy as np
 import pytest
@@ -278,6 +279,45 @@ def test_marshal_module_belongs_to_one_torch_and_python(monkeypatch):
     assert moe_build.marshal_up_to_date()
     monkeypatch.setattr(torch, "__version__", "0.0.0+other")
     assert not moe_build.marshal_up_to_date()
+
+
+def test_two_processes_may_build_the_marshal_module_at_once(monkeypatch, tmp_path):
+    # each compiles to a file of its own and puts the whole of it in place: the second
+    # process here builds while the compiler of the first is running
+    target = str(tmp_path / "module.so")
+    monkeypatch.setattr(moe_build, "marshal_file", lambda: target)
+    written = []
+
+    def compiler(cmd, check):
+        assert check
+        out = cmd[cmd.index("-o") + 1]
+        assert os.path.dirname(out) == str(tmp_path) and not os.path.exists(out)
+        with open(out, "w") as f:
+            f.write("first half, ")
+            f.flush()
+            written.append(out)
+            if len(written) == 1:
+                moe_build.build_marshal(force=True)
+                assert open(target).read() == "first half, second half"
+            f.write("second half")
+
+    monkeypatch.setattr(moe_build.subprocess, "run", compiler)
+    assert moe_build.build_marshal(force=True) == target
+    assert open(target).read() == "first half, second half" and len(written) == 2
+    assert os.listdir(tmp_path) == ["module.so"]
+
+
+def test_a_failed_build_of_the_marshal_module_leaves_nothing(monkeypatch, tmp_path):
+    monkeypatch.setattr(moe_build, "marshal_file", lambda: str(tmp_path / "module.so"))
+
+    def compiler(cmd, check):
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        raise RuntimeError("no compiler")
+
+    monkeypatch.setattr(moe_build.subprocess, "run", compiler)
+    with pytest.raises(RuntimeError):
+        moe_build.build_marshal(force=True)
+    assert os.listdir(tmp_path) == []
 
 
 # ---- the plain forms themselves ---------------------------------------------
