@@ -483,6 +483,10 @@ def moe_forward_scored(hidden, logits, bias, router: Router, w_gu, w_gu_scales, 
     T, H, _, E, _, fmt, _ = _dims(sh)
     if fmt not in _WEIGHT_ROWS:
         raise MoeError(1, "moe_forward_scored")
+    if ws.dtype is not U8:
+        if not ws.is_contiguous():
+            raise ValueError("tensors passed to libmoe_b200 must be contiguous")
+        ws = ws.unsqueeze(0).view(U8)
     spec = (hidden, T * H, _BF16, logits, T * E, _BF16 if router.logits else _F32, bias, E, _F32,
             *_weights(sh, w_gu, w_gu_scales, w_d, w_d_scales), out, T * H, _BF16, ws, 0, _U8)
     ph, pl, pb, pg, pgs, pd, pds, po, pws = _checked(d, *spec) or _addresses(d, *spec)

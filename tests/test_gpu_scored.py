@@ -308,6 +308,22 @@ def test_forward_scored_equals_its_steps(what, cfg, kw, biased):
     assert np.array_equal(bf16_bits(step), bf16_bits(out))
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.int64, torch.bfloat16])
+def test_forward_scored_takes_a_workspace_of_any_type(dtype):
+    cfg = moe_synth.MoeConfig("s6", T=24, H=256, I=128, E=16, k=4)
+    d = {n: t.to(DEV) for n, t in moe_synth.gen_inputs(cfg, seed=4).items()}
+    r, sh = moe.Router.of("sigmoid"), moe.Shape.of(cfg.T, cfg.H, cfg.I, cfg.E, cfg.k)
+    ref = moe.forward(d["hidden"], d["logits"], d["w_gu"], d["w_d"], cfg.k, router=r)
+    size = moe.moe_workspace_size(sh)
+    ws = torch.zeros(-(-size // dtype.itemsize), dtype=dtype, device=DEV)
+    out = torch.empty_like(ref)
+    moe.moe_forward_scored(d["hidden"], d["logits"], None, r, d["w_gu"], None, d["w_d"], None, sh, out, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(out.view(torch.int16), ref.view(torch.int16))
+    with pytest.raises(moe.MoeError, match="WORKSPACE"):
+        moe.moe_forward_scored(d["hidden"], d["logits"], None, r, d["w_gu"], None, d["w_d"], None, sh, out, ws[:8])
+
+
 def test_binding_refuses_another_device_and_host_memory():
     sh, r = moe.Shape.of(4, 128, 64, 8, 2), moe.Router.of()
     ids, w = torch.empty(4, 2, dtype=torch.int32, device=DEV), torch.empty(4, 2, device=DEV)

@@ -267,6 +267,17 @@ def test_int8_layer_refuses_short_activations(library_not_reached):
             moe.moe_forward(hidden, logits, w_gu, gs, w_d, ds, sh, out, ws, stream=0)
 
 
+@pytest.mark.parametrize("ws", [torch.zeros(1 << 18), torch.zeros(1 << 17, 2, dtype=torch.int64), torch.tensor(1.0)],
+                         ids=["fp32", "int64", "0-d"])
+def test_forward_scored_takes_a_workspace_of_any_type(library_not_reached, ws):
+    # as moe_forward does: what is refused here is the host memory
+    with pytest.raises(ValueError, match="current CUDA device"):
+        moe.moe_forward_scored(A, A, None, router(), A, None, A, None, moe.Shape.of(*LAYER), A, ws, stream=0)
+    strided = torch.zeros(4, 8)[:, ::2]
+    with pytest.raises(ValueError, match="contiguous"):
+        moe.moe_forward_scored(A, A, None, router(), A, None, A, None, moe.Shape.of(*LAYER), A, strided, stream=0)
+
+
 def test_router_struct_has_the_c_layout():
     assert [f[0] for f in moe.Router._fields_] == ["logits", "score", "n_group", "topk_group", "group_top",
                                                    "renormalize", "scale"]
