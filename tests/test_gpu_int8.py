@@ -332,6 +332,33 @@ def test_kernel_boundaries(T):
     check(case(T, 144, 80, 1, 1, seed=T))
 
 
+@pytest.mark.parametrize("T,H,I,E,k", [(1, 2048, 768, 8, 8), (16, 272, 144, 4, 2), (40, 512, 256, 8, 3), (64, 144, 80, 4, 1)])
+def test_the_three_kernels_give_the_same_bits(T, H, I, E, k):
+    """The same rows of the same experts in calls of 65 tokens and more, whose other
+    rows go to one more expert: at most 64 tokens and 16 rows per expert take the
+    warp kernel, more than 48 rows per expert the pair kernel, those between the
+    single-CTA one."""
+    c = case(T, H, I, E, k, seed=5)
+    P, src = c["P"], c["perm"].long() // k
+    a, a_s = c["hq"][src].contiguous(), c["hs"][src].contiguous()
+    assert P <= 16 * E and (min(E, P) * 2 * I * H) <= 32 << 20
+    y, act = down(c), gate_up(c, a, a_s, None)
+    g = torch.Generator(device=DEV).manual_seed(6)
+    more = lambda t, extra: torch.cat([t, extra])
+    for T2, per_expert in ((65, 30), (400, 60)):
+        P2 = T2 * k
+        X = max(1, P2 // per_expert - E)                              # more experts, all but the last without rows
+        assert P2 / (E + X) <= 48 if per_expert == 30 else P2 / (E + X) > 48
+        d = {"shape": moe.Shape.of(T2, H, I, E + X, k, "int8"), "P": P2,
+             "off": more(c["off"], torch.tensor([P] * (X - 1) + [P2], dtype=torch.int32, device=DEV)),
+             "w_gu": more(c["w_gu"], codes(g, X, 2 * I, H)), "gs": more(c["gs"], scales(g, X, 2 * I) * 1e-3),
+             "w_d": more(c["w_d"], codes(g, X, H, I)), "ds": more(c["ds"], scales(g, X, H)),
+             "aq": more(c["aq"], codes(g, P2 - P, I)), "as": more(c["as"], scales(g, P2 - P))}
+        assert torch.equal(down(d)[:P].view(torch.int16), y.view(torch.int16))
+        a2, a2_s = more(a, codes(g, P2 - P, H)), more(a_s, scales(g, P2 - P) * 1e-2)
+        assert torch.equal(gate_up(d, a2, a2_s, None)[:P].view(torch.int16), act.view(torch.int16))
+
+
 # ---- the layer ----------------------------------------------------------------
 
 def layer_inputs(T, H, I, E, k, seed=0, n_shared=0):
