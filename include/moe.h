@@ -146,7 +146,8 @@ MOE_API moe_status_t moe_route(const float *logits, const moe_shape_t *shape,
  *                      renormalize is 1, scale * s_j when it is 0: the bias
  *                      does not enter. A selected expert whose bias is -inf
  *                      (or NaN) has weight 0, and when the selected scores
- *                      are all 0 so are the weights.
+ *                      are all 0 so are the weights. (Any other bias counts as
+ *                      the number it is; as a mask -inf is also the fast one.)
  * Shared slots follow with weight 1, not scaled.
  *   1 <= topk_group <= n_group <= 32, E a multiple of n_group, group_top <=
  *   E / n_group (with more than one group), top_k <= topk_group * E / n_group,
@@ -387,7 +388,8 @@ MOE_API moe_status_t moe_i8_quantize(const moe_bf16_t *x, int32_t rows, int32_t 
  *                  through perm (TMA gather4)
  *   w_gu [E,2I,H] int8 (rows [0,I) gate, [I,2I) up), w_gu_scales [E,2I] fp32
  *   act [T*top_k, I] bf16 out: act = bf16(silu(g) * u), g and u the int32 sums
- *   times the weight row's scale and the token row's scale in fp32. */
+ *   times the weight row's scale and the token row's scale in fp32, silu within
+ *   2^-20 (1 + |g|), 0 below g = -87.3. */
 MOE_API moe_status_t moe_grouped_gemm_swiglu_i8(const int8_t *a_q, const float *a_scales, const int32_t *perm,
                                                 const int32_t *offsets, const void *w_gu, const void *w_gu_scales,
                                                 const moe_shape_t *shape, moe_bf16_t *act, moe_stream_t stream);

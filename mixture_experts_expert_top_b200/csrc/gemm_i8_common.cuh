@@ -1,6 +1,7 @@
 // gemm_i8_common.cuh -- pieces shared by the int8 grouped-GEMM kernels
-// (gemm_i8_sm100.cu: few tokens per expert; gemm_i8_pair_sm100.cu: many):
-// parameters and the epilogue's arithmetic, which must be the same in both.
+// (gemm_i8_warp_sm100.cu: few tokens per expert; gemm_i8_sm100.cu: middling
+// numbers; gemm_i8_pair_sm100.cu: many): parameters and the epilogue's
+// arithmetic, which must be the same in all three.
 #pragma once
 
 #include "gemm_common.cuh"
@@ -103,8 +104,8 @@ __device__ __forceinline__ uint32_t i8_bf16x2(float lo, float hi) {
 
 // silu(g) * u = g / (1 + exp(-g)) * u with the approximate exponential and
 // reciprocal (2^-22 and 2^-23, and 2^-23 |g| for the exponential's argument):
-// within 2^-20 (1 + |g|), below the bf16 rounding's 2^-8. exp(-g) past the fp32
-// range gives 0.
+// within 2^-20 (1 + |g|), below the bf16 rounding's 2^-8. Below g = -87.3, where
+// silu(g) is under 2^-119, the reciprocal leaves the normal range and gives 0.
 __device__ __forceinline__ float i8_act(float g, float u) {
     float e, r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.44269504f));
