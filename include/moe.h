@@ -166,8 +166,8 @@ typedef struct {
 
 /* logits [T,E] fp32 or bf16 (router->logits), bias [E] fp32 or NULL; topk_ids
  * and topk_w as moe_route's. One warp per token; weights in fp32 (expf, a
- * sigmoid's reciprocal within 2^-23, sum in slot order), each right to fp32
- * rounding down to the smallest normal number. */
+ * sigmoid's reciprocal within 2^-23, sum in slot order); no score or weight
+ * within the fp32 range is flushed to 0. */
 MOE_API moe_status_t moe_route_scored(const void *logits, const float *bias, const moe_router_t *router,
                                       const moe_shape_t *shape, int32_t *topk_ids, float *topk_w,
                                       moe_stream_t stream);

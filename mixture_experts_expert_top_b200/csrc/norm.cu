@@ -170,6 +170,7 @@ __device__ __forceinline__ Sum square_sum(const float (&h)[V][8], float f) {
                 lo = add2(lo, fma2(x, x, fma2(t, {-1.0f, -1.0f}, s)));
                 s = t;
             }
+        // past the fp32 range, or with a NaN, s says so and lo may be NaN
         const Sum sum = static_cast<Sum>(s.x) + s.y;
         return sum <= 2.0 * FLT_MAX ? sum - 2.0 * first + (lo.x + lo.y) : sum;
     } else {
